@@ -16,7 +16,8 @@ import torch
 __all__ = ["CkdaError", "library_path", "abi_version", "qk_prologue", "workspace_bytes",
            "fwd_chunked", "varlen_workspace_bytes", "fwd_varlen", "decode_step", "selftest_umma",
            "last_device_status", "set_wait_limit_ns", "bwd_workspace_bytes", "bwd_chunked",
-           "PATHS"]
+           "linattn_fwd_workspace_bytes", "linattn_fwd_chunked", "linattn_bwd_workspace_bytes",
+           "linattn_bwd_chunked", "linattn_decode_step", "PATHS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libckda.so")
@@ -85,6 +86,18 @@ def _load():
     lib.ckda_bwd_workspace_bytes.argtypes = [I, I, I, I, I]
     lib.ckda_bwd_chunked.restype = I
     lib.ckda_bwd_chunked.argtypes = [P] * 14 + [I] * 5 + [_Flags, I, LL, P, SZ, P]
+    lib.ckda_linattn_fwd_workspace_bytes.restype = SZ
+    lib.ckda_linattn_fwd_workspace_bytes.argtypes = [I, I, P, I, I, I, I]
+    lib.ckda_linattn_fwd_chunked.restype = I
+    lib.ckda_linattn_fwd_chunked.argtypes = [P, P, P, P, I, P, P, P, I, I, P, P, I, I, I, I, _Flags,
+                                             I, P, SZ, P]
+    lib.ckda_linattn_bwd_workspace_bytes.restype = SZ
+    lib.ckda_linattn_bwd_workspace_bytes.argtypes = [I, I, P, I, I, I, I, I]
+    lib.ckda_linattn_bwd_chunked.restype = I
+    lib.ckda_linattn_bwd_chunked.argtypes = [P, P, P, P, I] + [P] * 8 + [I, I, P, P, I, I, I, I,
+                                                                       _Flags, I, P, SZ, P]
+    lib.ckda_linattn_decode_step.restype = I
+    lib.ckda_linattn_decode_step.argtypes = [P, P, P, P, I, P, P, I, I, I, I, _Flags, I, P]
     lib.ckda_last_device_status.restype = I
     lib.ckda_last_device_status.argtypes = [P, ctypes.POINTER(I)]
     lib.ckda_set_wait_limit_ns.restype = I
@@ -433,6 +446,197 @@ def bwd_chunked(q, k, v, alpha, beta, h0, dout, dhT=None, *, l2norm=True, rope_t
         _dtype_code(q), int(pos_offset), _ptr(workspace), wbytes, _stream(q.device))
     _raise("ckda_bwd_chunked", st)
     return g
+
+
+class _on:
+    """The current device for a call whose tensors are on `device`."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def _linattn_shapes(q, k, v, log_decay, cu_seqlens, cu_seqlens_cpu):
+    """(B, T, n, lead, H, Hk, dk, dv, per_token, host offsets) of the chunked calls' arguments."""
+    _check(q, "q")
+    dev = q.device
+    _check(v, "v", dtype=q.dtype)
+    packed = cu_seqlens is not None
+    if not packed and q.dim() != 4:
+        raise ValueError(f"q: expected [B, T, Hk, dk], got {tuple(q.shape)}")
+    if packed and q.dim() not in (3, 4):
+        raise ValueError(f"q: expected [T, Hk, dk] or [1, T, Hk, dk], got {tuple(q.shape)}")
+    if packed and q.dim() == 4 and q.shape[0] != 1:
+        raise ValueError("packed sequences take a batch axis of 1 (or none)")
+    lead = tuple(q.shape[:-2])
+    if v.dim() != q.dim() or tuple(v.shape[:-2]) != lead:
+        raise ValueError(f"v: expected {lead + ('H', 'dv')}, got {tuple(v.shape)}")
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"v has {H} heads, not a multiple of q's {Hk}")
+    _check(k, "k", dtype=q.dtype, shape=q.shape)
+    per_token = log_decay.dim() != 1
+    _check(log_decay, "log_decay", dtype=torch.float32, shape=lead + (H,) if per_token else (H,))
+    host = None
+    if packed:
+        host = _host_offsets(cu_seqlens, cu_seqlens_cpu)
+        if int(host[-1]) != lead[-1]:
+            raise ValueError(f"cu_seqlens ends at {int(host[-1])}, but the token axis holds {lead[-1]}")
+        B, T, n = 1, lead[-1], host.numel() - 1
+    else:
+        B, T = lead
+        n = B
+    for t, name in ((k, "k"), (v, "v"), (log_decay, "log_decay"), (cu_seqlens, "cu_seqlens")):
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+    return B, T, n, lead, H, Hk, dk, dv, per_token, host
+
+
+def _on_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+
+
+def linattn_fwd_workspace_bytes(B, T, H, dk, dv, cu_seqlens_cpu=None) -> int:
+    """Device workspace bytes of linattn_fwd_chunked: B rows of T tokens, or (B and T ignored)
+    packed sequences with these host offsets.  0 when none is needed."""
+    host = None if cu_seqlens_cpu is None else cu_seqlens_cpu.to(torch.int32).contiguous()
+    n = _load().ckda_linattn_fwd_workspace_bytes(B, T, _ptr(host),
+                                                 0 if host is None else host.numel() - 1, H, dk, dv)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported problem for ckda_linattn_fwd_chunked")
+    return int(n)
+
+
+def linattn_fwd_chunked(q, k, v, log_decay, h0=None, *, cu_seqlens=None, cu_seqlens_cpu=None,
+                        scale=0.0, want_state=True, out=None, hT=None, workspace=None):
+    """Chunked linear attention with a decay for each head:
+    S_t = exp(log_decay_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.  Returns (out, hT or None).
+
+    q, k: [B, T, Hk, dk] (bf16 or fp32); v: [B, T, H, dv] same dtype, H a multiple of Hk (value
+    head h reads q/k head h // (H // Hk)); log_decay: fp32, [B, T, H] or [H] (fixed per head),
+    <= 0, -inf resets the state; h0 / hT: [B, H, dk, dv] fp32.  With cu_seqlens (int32 [n + 1] on
+    the device; cu_seqlens_cpu the same on the host, read back when omitted) the token axis holds n
+    packed sequences: [T, ..] or [1, T, ..] inputs, h0 / hT [n, H, dk, dv].  q and k are used as
+    they are (qk_prologue rotates and normalises them).
+    """
+    B, T, n, lead, H, Hk, dk, dv, per_token, host = _linattn_shapes(q, k, v, log_decay, cu_seqlens,
+                                                                    cu_seqlens_cpu)
+    dev = q.device
+    if h0 is not None:
+        _check(h0, "h0", dtype=torch.float32, shape=(n, H, dk, dv))
+    if out is None:
+        out = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
+    else:
+        _check(out, "out", dtype=q.dtype, shape=lead + (H, dv))
+    if hT is not None:
+        _check(hT, "hT", dtype=torch.float32, shape=(n, H, dk, dv))
+    elif want_state:
+        hT = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
+    if workspace is None:   # (a workspace given is checked against the need by the library)
+        need = linattn_fwd_workspace_bytes(B, T, H, dk, dv, host)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _on_device(dev, h0=h0, out=out, hT=hT, workspace=workspace)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(dev):
+        st = _load().ckda_linattn_fwd_chunked(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), _ptr(h0), _ptr(out),
+            _ptr(hT), B, T, _ptr(cu_seqlens), _ptr(host), n if host is not None else 0, H, dk, dv,
+            _flags(False, 0.0, 0, scale, qk_heads=Hk if Hk != H else 0), _dtype_code(q),
+            _ptr(workspace), wbytes, _stream(dev))
+    _raise("ckda_linattn_fwd_chunked", st)
+    return out, hT
+
+
+def linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv, cu_seqlens_cpu=None) -> int:
+    """Device workspace bytes of linattn_bwd_chunked (arguments as the forward's query)."""
+    host = None if cu_seqlens_cpu is None else cu_seqlens_cpu.to(torch.int32).contiguous()
+    n = _load().ckda_linattn_bwd_workspace_bytes(B, T, _ptr(host),
+                                                 0 if host is None else host.numel() - 1, H, Hk, dk,
+                                                 dv)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported problem for ckda_linattn_bwd_chunked")
+    return int(n)
+
+
+def linattn_bwd_chunked(q, k, v, log_decay, h0, dout, dhT=None, *, cu_seqlens=None,
+                        cu_seqlens_cpu=None, scale=0.0, want_dlog_decay=True, want_dh0=True,
+                        workspace=None):
+    """Gradients of <dout, out> + <dhT, hT> for linattn_fwd_chunked with the same inputs.
+
+    Returns a dict: dq, dk, dv in the inputs' dtype and layouts (a grouped q/k head receives the
+    sum over its value heads), dlog_decay (fp32, log_decay's shape) and dh0 (fp32); the last two
+    are None when not wanted.  dout has out's dtype and layout, dhT is fp32 or None.
+    """
+    B, T, n, lead, H, Hk, dk, dv, per_token, host = _linattn_shapes(q, k, v, log_decay, cu_seqlens,
+                                                                    cu_seqlens_cpu)
+    dev = q.device
+    _check(dout, "dout", dtype=q.dtype, shape=lead + (H, dv))
+    if h0 is not None:
+        _check(h0, "h0", dtype=torch.float32, shape=(n, H, dk, dv))
+    if dhT is not None:
+        _check(dhT, "dhT", dtype=torch.float32, shape=(n, H, dk, dv))
+    g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+         "dlog_decay": torch.empty_like(log_decay) if want_dlog_decay else None,
+         "dh0": torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None}
+    if workspace is None:
+        workspace = torch.empty(linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv, host),
+                                dtype=torch.uint8, device=dev)
+    _on_device(dev, h0=h0, dout=dout, dhT=dhT, workspace=workspace)
+    wbytes = workspace.numel() * workspace.element_size()
+    with _on(dev):
+        st = _load().ckda_linattn_bwd_chunked(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), _ptr(h0), _ptr(dout),
+            _ptr(dhT), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dlog_decay"]),
+            _ptr(g["dh0"]), B, T, _ptr(cu_seqlens), _ptr(host), n if host is not None else 0, H, dk,
+            dv, _flags(False, 0.0, 0, scale, qk_heads=Hk if Hk != H else 0), _dtype_code(q),
+            _ptr(workspace), wbytes, _stream(dev))
+    _raise("ckda_linattn_bwd_chunked", st)
+    return g
+
+
+def linattn_decode_step(q, k, v, log_decay, state, *, scale=0.0, out=None):
+    """One token of the linear attention for N sequences, in place on state [N, H, dk, dv] fp32:
+    S <- exp(log_decay) S + k v^T, out = scale S^T q [N, H, dv].  q, k: [N, Hk, dk]; v: [N, H, dv];
+    log_decay: fp32 [N, H] or [H]."""
+    _check(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q: expected [N, Hk, dk], got {tuple(q.shape)}")
+    N, Hk, dk = q.shape
+    _check(v, "v", dtype=q.dtype)
+    if v.dim() != 3 or v.shape[0] != N:
+        raise ValueError(f"v: expected [N={N}, H, dv], got {tuple(v.shape)}")
+    H, dv = v.shape[1], v.shape[2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"v has {H} heads, not a multiple of q's {Hk}")
+    dev = q.device
+    _check(k, "k", dtype=q.dtype, shape=q.shape)
+    per_token = log_decay.dim() != 1
+    _check(log_decay, "log_decay", dtype=torch.float32, shape=(N, H) if per_token else (H,))
+    _check(state, "state", dtype=torch.float32, shape=(N, H, dk, dv))
+    if out is None:
+        out = torch.empty((N, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _check(out, "out", dtype=q.dtype, shape=(N, H, dv))
+    _on_device(dev, k=k, v=v, log_decay=log_decay, state=state, out=out)
+    with _on(dev):
+        st = _load().ckda_linattn_decode_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), _ptr(state), _ptr(out), N,
+            H, dk, dv, _flags(False, 0.0, 0, scale, qk_heads=Hk if Hk != H else 0), _dtype_code(q),
+            _stream(dev))
+    _raise("ckda_linattn_decode_step", st)
+    return out
 
 
 def last_device_status(device=None) -> int:

@@ -1,0 +1,218 @@
+// linattn_api.cu -- the C ABI of the decayed linear attention: argument validation and dispatch.
+// Everything here runs on the host before any launch; nothing is allocated.
+#include <math.h>
+
+#include "linattn.cuh"
+
+using namespace ckda;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+size_t elem_size(ckda_dtype t) { return t == CKDA_BF16 ? 2 : 4; }
+ckda_status from_cuda(cudaError_t e) { return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA; }
+
+struct Buf { const void* p; size_t n; };
+bool overlap(const Buf& a, const Buf& b) {
+    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.n && y < x + a.n;
+}
+
+// The token axis: B rows of T tokens, or n packed sequences.
+struct Tokens {
+    int n, T;              // sequences; tokens of a row (batched) or of the axis (packed)
+    long long total, longest;
+};
+ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tokens* t) {
+    if (!cu_host) {
+        if (B < 1 || T < 1 || H < 1) return CKDA_ERR_SHAPE;
+        *t = Tokens{B, T, (long long)B * T, T};
+    } else {
+        if (n_seqs < 1 || H < 1) return CKDA_ERR_SHAPE;
+        if (cu_host[0] != 0) return CKDA_ERR_ARG;
+        long long longest = 0;
+        for (int s = 0; s < n_seqs; ++s) {
+            const long long len = (long long)cu_host[s + 1] - cu_host[s];
+            if (len < 0) return CKDA_ERR_ARG;
+            longest = len > longest ? len : longest;
+        }
+        *t = Tokens{n_seqs, cu_host[n_seqs], (long long)cu_host[n_seqs], longest};
+    }
+    // (grid sizes and chunk numbers stay below 2^31, byte counts below 2^48)
+    if (t->longest > 0x7fffff00ll) return CKDA_ERR_SHAPE;   // (rounded up to whole chunks below 2^31)
+    if ((t->total / kLaChunk + 2ll * t->n + 1) * H > 0x7fffffll * 16) return CKDA_ERR_SHAPE;
+    if (t->total > (1ll << 40) / 128 / H) return CKDA_ERR_SHAPE;
+    return CKDA_OK;
+}
+
+// Units that run side by side: two CTAs of the forward run fit an SM (148 SMs); of the backward's
+// one, with two or three runs sharing a launch.
+constexpr int kFwdSlots = 296, kBwdSlots = 148;
+
+LaSplit make_split(const Tokens& t, const int* cu, const int* cu_host, int H, int slots) {
+    LaSplit sp;
+    sp.cu = cu;
+    sp.n = t.n;
+    sp.T = t.T;
+    sp.H = H;
+    sp.L = la_unit_len(t.total, t.longest, H, slots);
+    sp.units = (int)la_units(cu_host, t.n, t.T, sp.L);
+    return sp;
+}
+
+ckda_status check_flags(const ckda_flags& f, int H, int* G) {
+    // the rotation, the norm and gate logits belong to the CKDA recurrence and its prologue
+    if (f.l2norm || f.rope_theta > 0.f || f.gate_logits) return CKDA_ERR_ARG;
+    if (f.qk_heads < 0 || (f.qk_heads > 0 && H % f.qk_heads != 0)) return CKDA_ERR_ARG;
+    *G = f.qk_heads > 0 ? H / f.qk_heads : 1;
+    return CKDA_OK;
+}
+float resolve_scale(const ckda_flags& f, int dk) {
+    return f.scale != 0.f ? f.scale : (float)(1.0 / sqrt((double)dk));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ckda_linattn_fwd_workspace_bytes(int B, int T, const int* cu_seqlens_host, int n_seqs,
+                                        int H, int dk, int dv) {
+    Tokens t;
+    if (!supported_dim(dk) || !supported_dim(dv)) return (size_t)-1;
+    if (read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t) != CKDA_OK) return (size_t)-1;
+    return la_fwd_workspace(make_split(t, nullptr, cu_seqlens_host, H, kFwdSlots), t.longest, dk,
+                            dv);
+}
+
+ckda_status ckda_linattn_fwd_chunked(const void* q, const void* k, const void* v,
+                                     const float* log_decay, int per_token, const float* h0,
+                                     void* out, float* hT, int B, int T, const int* cu_seqlens,
+                                     const int* cu_seqlens_host, int n_seqs, int H, int dk, int dv,
+                                     ckda_flags flags, ckda_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, ckda_stream_t stream) {
+    if (!q || !k || !v || !log_decay || !out) return CKDA_ERR_NULL;
+    if (!cu_seqlens != !cu_seqlens_host) return CKDA_ERR_NULL;
+    if (dtype != CKDA_F32 && dtype != CKDA_BF16) return CKDA_ERR_UNSUPPORTED;
+    Tokens t;
+    ckda_status st = read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t);
+    if (st != CKDA_OK) return st;
+    if (!supported_dim(dk) || !supported_dim(dv)) return CKDA_ERR_UNSUPPORTED;
+    if (per_token != 0 && per_token != 1) return CKDA_ERR_ARG;
+    int G;
+    if ((st = check_flags(flags, H, &G)) != CKDA_OK) return st;
+    const void* ptrs[] = {q, k, v, h0, out, hT, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return CKDA_ERR_ALIGN;
+    if (!aligned4(cu_seqlens) || !aligned4(log_decay)) return CKDA_ERR_ALIGN;
+    const LaSplit sp = make_split(t, cu_seqlens, cu_seqlens_host, H, kFwdSlots);
+    const size_t need = la_fwd_workspace(sp, t.longest, dk, dv);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return CKDA_ERR_WORKSPACE;
+    const size_t es = elem_size(dtype), tok = (size_t)t.total, nst = (size_t)t.n * H * dk * dv * 4;
+    const Buf ins[] = {{q, tok * (H / G) * dk * es}, {k, tok * (H / G) * dk * es},
+                       {v, tok * H * dv * es}, {log_decay, (per_token ? tok * H : H) * 4},
+                       {h0, nst}, {cu_seqlens, ((size_t)t.n + 1) * 4}};
+    const Buf outs[] = {{out, tok * H * dv * es}, {hT, nst}, {need ? workspace : nullptr, need}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Buf& in : ins)
+            if (!(i == 1 && in.p == h0 && hT == h0) && overlap(outs[i], in)) return CKDA_ERR_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return CKDA_ERR_ARG;
+    }
+    const LaFwdArgs a{q, k, v, log_decay, h0, out, hT, per_token, G, resolve_scale(flags, dk), sp};
+    return from_cuda(launch_la_fwd(a, t.longest, dk, dv, dtype, workspace, (cudaStream_t)stream));
+}
+
+size_t ckda_linattn_bwd_workspace_bytes(int B, int T, const int* cu_seqlens_host, int n_seqs,
+                                        int H, int qk_heads, int dk, int dv) {
+    Tokens t;
+    if (!supported_dim(dk) || !supported_dim(dv)) return (size_t)-1;
+    if (read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t) != CKDA_OK) return (size_t)-1;
+    if (qk_heads < 0 || (qk_heads > 0 && H % qk_heads != 0)) return (size_t)-1;
+    return la_bwd_workspace(make_split(t, nullptr, cu_seqlens_host, H, kBwdSlots), t.longest,
+                            t.total, qk_heads > 0 ? H / qk_heads : 1, dk, dv);
+}
+
+ckda_status ckda_linattn_bwd_chunked(const void* q, const void* k, const void* v,
+                                     const float* log_decay, int per_token, const float* h0,
+                                     const void* dout, const float* dhT, void* dq, void* dk,
+                                     void* dv, float* dlog_decay, float* dh0, int B, int T,
+                                     const int* cu_seqlens, const int* cu_seqlens_host, int n_seqs,
+                                     int H, int dk_, int dv_, ckda_flags flags, ckda_dtype dtype,
+                                     void* workspace, size_t workspace_bytes,
+                                     ckda_stream_t stream) {
+    if (!q || !k || !v || !log_decay || !dout || !dq || !dk || !dv) return CKDA_ERR_NULL;
+    if (!cu_seqlens != !cu_seqlens_host) return CKDA_ERR_NULL;
+    if (dtype != CKDA_F32 && dtype != CKDA_BF16) return CKDA_ERR_UNSUPPORTED;
+    Tokens t;
+    ckda_status st = read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t);
+    if (st != CKDA_OK) return st;
+    if (!supported_dim(dk_) || !supported_dim(dv_)) return CKDA_ERR_UNSUPPORTED;
+    if (per_token != 0 && per_token != 1) return CKDA_ERR_ARG;
+    int G;
+    if ((st = check_flags(flags, H, &G)) != CKDA_OK) return st;
+    const void* ptrs[] = {q, k, v, h0, dout, dhT, dq, dk, dv, dh0, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return CKDA_ERR_ALIGN;
+    if (!aligned4(cu_seqlens) || !aligned4(log_decay) || !aligned4(dlog_decay))
+        return CKDA_ERR_ALIGN;
+    const LaSplit sp = make_split(t, cu_seqlens, cu_seqlens_host, H, kBwdSlots);
+    const size_t need = la_bwd_workspace(sp, t.longest, t.total, G, dk_, dv_);
+    if (!workspace || workspace_bytes < need) return CKDA_ERR_WORKSPACE;
+    const size_t es = elem_size(dtype), tok = (size_t)t.total;
+    const size_t nst = (size_t)t.n * H * dk_ * dv_ * 4, ng = (per_token ? tok * H : H) * 4;
+    const size_t nqk = tok * (H / G) * dk_ * es, nv = tok * H * dv_ * es;
+    const Buf ins[] = {{q, nqk}, {k, nqk}, {v, nv}, {log_decay, ng}, {h0, nst}, {dout, nv},
+                       {dhT, nst}, {cu_seqlens, ((size_t)t.n + 1) * 4}};
+    const Buf outs[] = {{dq, nqk}, {dk, nqk}, {dv, nv}, {dlog_decay, ng}, {dh0, nst},
+                        {workspace, need}};
+    for (int i = 0; i < 6; ++i) {
+        for (const Buf& in : ins)
+            if (overlap(outs[i], in)) return CKDA_ERR_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return CKDA_ERR_ARG;
+    }
+    LaBwdArgs a;
+    a.q = q; a.k = k; a.v = v; a.g = log_decay; a.h0 = h0; a.dout = dout; a.dhT = dhT;
+    a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dlog_decay; a.dh0 = dh0;
+    a.per_token = per_token;
+    a.G = G;
+    a.scale = resolve_scale(flags, dk_);
+    a.sp = sp;
+    a.tokens = t.total;
+    a.chunks = (int)la_units(cu_seqlens_host, t.n, t.T, kLaChunk);
+    return from_cuda(launch_la_bwd(a, t.longest, dk_, dv_, dtype, workspace,
+                                   (cudaStream_t)stream));
+}
+
+ckda_status ckda_linattn_decode_step(const void* q, const void* k, const void* v,
+                                     const float* log_decay, int per_token, float* state,
+                                     void* out, int N, int H, int dk, int dv, ckda_flags flags,
+                                     ckda_dtype dtype, ckda_stream_t stream) {
+    if (!q || !k || !v || !log_decay || !state || !out) return CKDA_ERR_NULL;
+    if (dtype != CKDA_F32 && dtype != CKDA_BF16) return CKDA_ERR_UNSUPPORTED;
+    if (N < 1 || H < 1) return CKDA_ERR_SHAPE;
+    if ((long long)N * H > (1ll << 26)) return CKDA_ERR_SHAPE;
+    if (!supported_dim(dk) || !supported_dim(dv)) return CKDA_ERR_UNSUPPORTED;
+    if (per_token != 0 && per_token != 1) return CKDA_ERR_ARG;
+    int G;
+    ckda_status st = check_flags(flags, H, &G);
+    if (st != CKDA_OK) return st;
+    const void* ptrs[] = {q, k, v, state, out};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return CKDA_ERR_ALIGN;
+    if (!aligned4(log_decay)) return CKDA_ERR_ALIGN;
+    const size_t es = elem_size(dtype), n = N;
+    const Buf ins[] = {{q, n * (H / G) * dk * es}, {k, n * (H / G) * dk * es}, {v, n * H * dv * es},
+                       {log_decay, (per_token ? n * H : H) * 4}};
+    const Buf o{out, n * H * dv * es}, s{state, n * H * dk * dv * 4};
+    for (const Buf& in : ins)
+        if (overlap(o, in) || overlap(s, in)) return CKDA_ERR_ARG;
+    if (overlap(o, s)) return CKDA_ERR_ARG;
+    return from_cuda(launch_la_decode(q, k, v, log_decay, per_token, state, out, N, H, G, dk, dv,
+                                      resolve_scale(flags, dk), dtype, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -336,6 +336,73 @@ CKDA_API ckda_status ckda_bwd_chunked(const void* q, const void* k, const void* 
                                       size_t workspace_bytes, ckda_stream_t stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrence without the delta rule,
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t,      S in R^{dk x dv},
+ * g_t a log decay per value head (<= 0; -inf makes the decay zero and so resets the state before
+ * the token).  Conventions as above; q and k are used as given (ckda_qk_prologue rotates and
+ * normalises them).
+ *   q, k      : [B, T, Hk, dk] dtype (Hk = flags.qk_heads, or H)     v, out : [B, T, H, dv] dtype
+ *   log_decay : fp32, [B, T, H] (per_token = 1) or [H] (per_token = 0: fixed decays); 4-byte
+               aligned, as is its gradient (every other array 16-byte)
+ *   h0, hT    : [B, H, dk, dv] fp32; h0 may be NULL (zero), hT NULL (not wanted) or equal to h0
+ *   cu_seqlens, cu_seqlens_host, n_seqs : packed sequences, as in ckda_fwd_varlen (both pointers,
+ *               or both NULL): then B and T are ignored, the token axis holds
+ *               cu_seqlens_host[n_seqs] tokens and h0, hT are [n_seqs, H, dk, dv].  Sequences may
+ *               be empty (hT is h0, or zero).  Offsets on the device that differ from the host's
+ *               give undefined results within the arrays.
+ *   flags     : scale and qk_heads are used, path and stages ignored; l2norm, rope_theta > 0 or
+ *               gate_logits: CKDA_ERR_ARG
+ *   workspace : ckda_linattn_fwd_workspace_bytes (0: may be NULL); not shared with concurrent
+ *               calls.
+ * Long sequences are cut into units of tokens worked on side by side: summaries of the units, a
+ * scan over them, then every unit from its entering state.  States are kept and updated with
+ * fp32-grade products for either type; with bf16 inputs the scores and the state are rounded to
+ * bf16 where they enter the output's products.  No positive exponent of a decay is formed, so any
+ * g <= 0 is safe; a growing g > 0 is accepted and can overflow as the recurrence does.  A
+ * non-finite input reaches every later output of its head, and may reach the outputs of earlier
+ * tokens of the same chunk of 64 (or 128) tokens.
+ */
+CKDA_API size_t ckda_linattn_fwd_workspace_bytes(int B, int T, const int* cu_seqlens_host,
+                                                 int n_seqs, int H, int dk, int dv);
+CKDA_API ckda_status ckda_linattn_fwd_chunked(
+    const void* q, const void* k, const void* v, const float* log_decay, int per_token,
+    const float* h0, void* out, float* hT, int B, int T, const int* cu_seqlens,
+    const int* cu_seqlens_host, int n_seqs, int H, int dk, int dv, ckda_flags flags,
+    ckda_dtype dtype, void* workspace, size_t workspace_bytes, ckda_stream_t stream);
+
+/*
+ * Backward of ckda_linattn_fwd_chunked: gradients of <dout, out> + <dhT, hT>.
+ *   dout : [B, T, H, dv] dtype          dhT : [B, H, dk, dv] fp32, or NULL for zero
+ *   dq, dk : [B, T, Hk, dk] dtype (a grouped q/k head receives the sum over its value heads)
+ *   dv   : [B, T, H, dv] dtype
+ *   dlog_decay : fp32, the shape of log_decay (fixed decays: the sum over all tokens), or NULL
+ *                to skip it; zero where exp(g) is zero
+ *   dh0  : fp32, or NULL to skip it
+ *   workspace : ckda_linattn_bwd_workspace_bytes (never 0), not shared with concurrent calls.
+ * Outputs must not overlap the inputs or each other; results do not depend on timing (no atomics).
+ */
+CKDA_API size_t ckda_linattn_bwd_workspace_bytes(int B, int T, const int* cu_seqlens_host,
+                                                 int n_seqs, int H, int qk_heads, int dk, int dv);
+CKDA_API ckda_status ckda_linattn_bwd_chunked(
+    const void* q, const void* k, const void* v, const float* log_decay, int per_token,
+    const float* h0, const void* dout, const float* dhT, void* dq, void* dk, void* dv,
+    float* dlog_decay, float* dh0, int B, int T, const int* cu_seqlens, const int* cu_seqlens_host,
+    int n_seqs, int H, int dk_, int dv_, ckda_flags flags, ckda_dtype dtype, void* workspace,
+    size_t workspace_bytes, ckda_stream_t stream);
+
+/*
+ * One token of the linear attention for N sequences, in place on the caller's fp32 state:
+ *   q, k : [N, Hk, dk]    v, out : [N, H, dv]    log_decay : fp32 [N, H] (per_token) or [H]
+ *   state : [N, H, dk, dv] fp32, overwritten with S_t = exp(g) S + k v^T; out = scale S_t^T q.
+ * flags as ckda_linattn_fwd_chunked.  The state is read once and written once.
+ */
+CKDA_API ckda_status ckda_linattn_decode_step(const void* q, const void* k, const void* v,
+                                              const float* log_decay, int per_token, float* state,
+                                              void* out, int N, int H, int dk, int dv,
+                                              ckda_flags flags, ckda_dtype dtype,
+                                              ckda_stream_t stream);
+
+/*
  * Diagnostic: D[M, N] (fp32, row-major) = A[M, K] * B for bf16 A (row-major, K contiguous),
  * computed by the library's own tcgen05 tensor-core wrappers (shared-memory operand
  * descriptors with the 128-byte swizzle, TMEM accumulator, one CTA).
