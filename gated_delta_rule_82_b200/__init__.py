@@ -17,7 +17,8 @@ __all__ = ["CkdaError", "library_path", "abi_version", "qk_prologue", "workspace
            "fwd_chunked", "varlen_workspace_bytes", "fwd_varlen", "decode_step", "selftest_umma",
            "last_device_status", "set_wait_limit_ns", "bwd_workspace_bytes", "bwd_chunked",
            "linattn_fwd_workspace_bytes", "linattn_fwd_chunked", "linattn_bwd_workspace_bytes",
-           "linattn_bwd_chunked", "linattn_decode_step", "PATHS"]
+           "linattn_bwd_chunked", "linattn_decode_step", "block_norm", "block_norm_bwd",
+           "block_norm_bwd_workspace_bytes", "PATHS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libckda.so")
@@ -39,6 +40,11 @@ class _Flags(ctypes.Structure):
                 ("rope_convention", ctypes.c_int), ("scale", ctypes.c_float),
                 ("path", ctypes.c_int), ("stages", ctypes.c_int), ("gate_logits", ctypes.c_int),
                 ("rope_dims", ctypes.c_int), ("qk_heads", ctypes.c_int)]
+
+
+class _NormFlags(ctypes.Structure):
+    _fields_ = [("post_group", ctypes.c_int), ("gate_act", ctypes.c_int),
+                ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -98,6 +104,12 @@ def _load():
                                                                        _Flags, I, P, SZ, P]
     lib.ckda_linattn_decode_step.restype = I
     lib.ckda_linattn_decode_step.argtypes = [P, P, P, P, I, P, P, I, I, I, I, _Flags, I, P]
+    lib.ckda_block_norm.restype = I
+    lib.ckda_block_norm.argtypes = [P] * 8 + [LL, I, _NormFlags, I, P]
+    lib.ckda_block_norm_bwd_workspace_bytes.restype = SZ
+    lib.ckda_block_norm_bwd_workspace_bytes.argtypes = [LL, I, I]
+    lib.ckda_block_norm_bwd.restype = I
+    lib.ckda_block_norm_bwd.argtypes = [P] * 14 + [LL, I, _NormFlags, I, P, SZ, P]
     lib.ckda_last_device_status.restype = I
     lib.ckda_last_device_status.argtypes = [P, ctypes.POINTER(I)]
     lib.ckda_set_wait_limit_ns.restype = I
@@ -637,6 +649,122 @@ def linattn_decode_step(q, k, v, log_decay, state, *, scale=0.0, out=None):
             _stream(dev))
     _raise("ckda_linattn_decode_step", st)
     return out
+
+
+GATE_ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+def _norm_args(y, gate, gate_act, residual, post_group, post_weight, res_scale, res_vector, eps,
+               pre_weight):
+    """(rows, D, flags) of the block norms' shared arguments."""
+    _check(y, "y")
+    if y.dim() < 1 or y.numel() == 0:
+        raise ValueError(f"y: expected [.., D] with at least one row, got {tuple(y.shape)}")
+    D = y.shape[-1]
+    for t, name in ((gate, "gate"), (residual, "residual")):
+        if t is not None:
+            _check(t, name, dtype=y.dtype, shape=y.shape)
+    if (gate is None) != (gate_act == "none"):
+        raise ValueError("gate and gate_act go together (gate_act 'none' without a gate)")
+    if post_weight is not None:
+        if not post_group:
+            raise ValueError("post_weight without a first norm (post_group = 0)")
+        _check(post_weight, "post_weight", dtype=torch.float32, shape=(post_group,))
+    for t, name in ((res_vector, "res_vector"), (pre_weight, "pre_weight")):
+        if t is not None:
+            _check(t, name, dtype=torch.float32, shape=(D,))
+    _on_device(y.device, gate=gate, residual=residual, post_weight=post_weight,
+               res_vector=res_vector, pre_weight=pre_weight)
+    return y.numel() // D, D, _NormFlags(int(post_group), GATE_ACTS[gate_act], float(res_scale),
+                                         float(eps))
+
+
+def block_norm(y, *, gate=None, gate_act="none", residual=None, post_group=0, post_weight=None,
+               res_scale=1.0, res_vector=None, pre_norm=False, pre_weight=None, eps=1e-5, h=None,
+               n=None):
+    """The norms around a block, fused with its gate, scale and the residual add, for y [.., D]:
+
+        u = rms_norm(y, over groups of post_group channels) * post_weight   (post_group 0: u = y)
+        h = residual + res_scale * res_vector * u * act(gate)
+        n = rms_norm(h, over D) * pre_weight                                 (with pre_norm)
+
+    Returns (h, n or None) in y's dtype (bf16 or fp32).  post_group: 0, D, or 16, 32, 64, 128
+    dividing D (a norm per head, one weight [post_group] for all); gate, residual: y's shape or
+    None; gate_act "sigmoid" or "silu" with a gate; weights fp32, None for ones.  An attention
+    head's output norm with its gate is block_norm(out.flatten(-2), post_group=dv, gate=..., ...).
+    """
+    rows, D, flags = _norm_args(y, gate, gate_act, residual, post_group, post_weight, res_scale,
+                                res_vector, eps, pre_weight)
+    if pre_weight is not None and not pre_norm:
+        raise ValueError("pre_weight without pre_norm")
+    if n is not None and not pre_norm:
+        raise ValueError("n without pre_norm")
+    if h is None:
+        h = torch.empty_like(y)
+    else:
+        _check(h, "h", dtype=y.dtype, shape=y.shape)
+    if pre_norm:
+        if n is None:
+            n = torch.empty_like(y)
+        else:
+            _check(n, "n", dtype=y.dtype, shape=y.shape)
+    _on_device(y.device, h=h, n=n)
+    with _on(y.device):
+        st = _load().ckda_block_norm(_ptr(y), _ptr(gate), _ptr(residual), _ptr(post_weight),
+                                     _ptr(res_vector), _ptr(pre_weight), _ptr(h), _ptr(n), rows, D,
+                                     flags, _dtype_code(y), _stream(y.device))
+    _raise("ckda_block_norm", st)
+    return h, n
+
+
+def block_norm_bwd_workspace_bytes(rows, D, post_group=0) -> int:
+    n = _load().ckda_block_norm_bwd_workspace_bytes(rows, D, post_group)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("unsupported problem for ckda_block_norm_bwd")
+    return int(n)
+
+
+def block_norm_bwd(y, dh, dn=None, *, gate=None, gate_act="none", residual=None, post_group=0,
+                   post_weight=None, res_scale=1.0, res_vector=None, pre_norm=False,
+                   pre_weight=None, eps=1e-5, workspace=None):
+    """Gradients of <dh, h> + <dn, n> for block_norm with the same arguments (dh or dn may be None,
+    not both; dn only with pre_norm).
+
+    Returns a dict: dy, and dgate and dresidual where there is a gate and a residual, in y's dtype;
+    dpost_weight, dres_vector and dpre_weight (fp32) where those vectors were given; else None.
+    """
+    rows, D, flags = _norm_args(y, gate, gate_act, residual, post_group, post_weight, res_scale,
+                                res_vector, eps, pre_weight)
+    if dn is not None and not pre_norm:
+        raise ValueError("dn without pre_norm")
+    if dh is None and dn is None:
+        raise ValueError("dh and dn are both missing")
+    if pre_weight is not None and not pre_norm:
+        raise ValueError("pre_weight without pre_norm")
+    for t, name in ((dh, "dh"), (dn, "dn")):
+        if t is not None:
+            _check(t, name, dtype=y.dtype, shape=y.shape)
+    _on_device(y.device, dh=dh, dn=dn, workspace=workspace)
+    like = lambda t: None if t is None else torch.empty_like(t)
+    g = {"dy": torch.empty_like(y), "dgate": like(gate), "dresidual": like(residual),
+         "dpost_weight": like(post_weight), "dres_vector": like(res_vector), "dpre_weight": None}
+    if pre_weight is not None:
+        g["dpre_weight"] = torch.empty_like(pre_weight) if dn is not None else \
+            torch.zeros_like(pre_weight)
+    sums = post_weight is not None or res_vector is not None or pre_weight is not None
+    if workspace is None and sums:
+        workspace = torch.empty(block_norm_bwd_workspace_bytes(rows, D, post_group),
+                                dtype=torch.uint8, device=y.device)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(y.device):
+        st = _load().ckda_block_norm_bwd(
+            _ptr(y), _ptr(gate), _ptr(residual), _ptr(post_weight), _ptr(res_vector),
+            _ptr(pre_weight), _ptr(dh), _ptr(dn), _ptr(g["dy"]), _ptr(g["dgate"]),
+            _ptr(g["dresidual"]), _ptr(g["dpost_weight"]), _ptr(g["dres_vector"]),
+            _ptr(g["dpre_weight"]) if dn is not None else None, rows, D, flags, _dtype_code(y),
+            _ptr(workspace), wbytes, _stream(y.device))
+    _raise("ckda_block_norm_bwd", st)
+    return g
 
 
 def last_device_status(device=None) -> int:

@@ -403,6 +403,59 @@ CKDA_API ckda_status ckda_linattn_decode_step(const void* q, const void* k, cons
                                               ckda_stream_t stream);
 
 /*
+ * The norms around a block, fused with its gate, its scale and the residual add.  For `rows` rows
+ * of D channels (every array dense [rows, D] of `dtype`; arithmetic in fp32):
+ *     u = y * rsqrt(mean over the group of y^2 + eps) * post_weight   (post_group channels a group)
+ *     m = u * act(gate),   h = residual + res_scale * res_vector * m
+ *     n = h * rsqrt(mean over the row of h^2 + eps) * pre_weight
+ *   y          : the block's output (an attention head's, with post_group = dv, or a whole row)
+ *   post_group : 0 = no norm of y; D = over the row; or 16, 32, 64, 128 dividing D: per group,
+ *                each with the same post_weight[post_group] (the norm of every head)
+ *   gate       : NULL = no gate (gate_act must be 0); gate_act 1 = logistic, 2 = x * logistic(x)
+ *   residual   : NULL = zero          res_vector : fp32 [D], NULL = ones
+ *   h          : written              n : written, or NULL for no second norm
+ *   weights    : fp32, NULL = ones; 4-byte aligned (the [rows, D] arrays 16-byte)
+ * 1 <= D <= 8192, eps > 0.  n is formed from h before h is rounded to `dtype`.  h may equal
+ * residual or y, and n may equal y or gate (each element is read before it is written).
+ */
+#define CKDA_BLOCK_NORM_MAX_D 8192
+typedef struct {
+    int post_group;
+    int gate_act;        /* 0 none, 1 logistic, 2 x * logistic(x) */
+    float res_scale;
+    float eps;
+} ckda_norm_flags;
+
+CKDA_API ckda_status ckda_block_norm(const void* y, const void* gate, const void* residual,
+                                     const float* post_weight, const float* res_vector,
+                                     const float* pre_weight, void* h, void* n, long long rows,
+                                     int D, ckda_norm_flags flags, ckda_dtype dtype,
+                                     ckda_stream_t stream);
+
+/*
+ * Backward of ckda_block_norm: gradients of <dh, h> + <dn, n>, from the forward's inputs alone
+ * (its statistics are formed again, in fp32).
+ *   dh, dn : [rows, D] dtype, either may be NULL (zero) but not both; dn NULL: the forward without
+ *            the second norm
+ *   dy     : [rows, D] dtype               dgate : the same, required with a gate
+ *   dresidual : [rows, D] dtype, or NULL to skip it (the gradient of h through both paths)
+ *   dpost_weight [post_group], dres_vector [D], dpre_weight [D] : fp32, NULL to skip; summed over
+ *            the rows in a fixed order (no atomics)
+ *   workspace : ckda_block_norm_bwd_workspace_bytes, needed only with one of those three; not
+ *            shared with concurrent calls.
+ * dy, dgate and dresidual may each equal dh or dn, or y, gate and residual in this order.
+ */
+CKDA_API size_t ckda_block_norm_bwd_workspace_bytes(long long rows, int D, int post_group);
+CKDA_API ckda_status ckda_block_norm_bwd(const void* y, const void* gate, const void* residual,
+                                         const float* post_weight, const float* res_vector,
+                                         const float* pre_weight, const void* dh, const void* dn,
+                                         void* dy, void* dgate, void* dresidual,
+                                         float* dpost_weight, float* dres_vector,
+                                         float* dpre_weight, long long rows, int D,
+                                         ckda_norm_flags flags, ckda_dtype dtype, void* workspace,
+                                         size_t workspace_bytes, ckda_stream_t stream);
+
+/*
  * Diagnostic: D[M, N] (fp32, row-major) = A[M, K] * B for bf16 A (row-major, K contiguous),
  * computed by the library's own tcgen05 tensor-core wrappers (shared-memory operand
  * descriptors with the 128-byte swizzle, TMEM accumulator, one CTA).
