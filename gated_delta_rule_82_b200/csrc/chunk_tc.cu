@@ -56,6 +56,7 @@
 #include "fastdiv.h"
 #include "lanes.h"
 #include "internal.cuh"
+#include "linattn.cuh"
 #include "tc_sm100.cuh"
 
 namespace ckda {
@@ -2217,7 +2218,9 @@ cudaError_t device_status_take(cudaStream_t stream, int* code) {
                                     stream);
         if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     }
-    *code = v;
+    int la = 0;      // (the linear attention's word)
+    if (e == cudaSuccess) e = la_status_take(stream, &la);
+    *code = v ? v : la;
     return e;
 }
 

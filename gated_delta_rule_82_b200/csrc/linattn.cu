@@ -610,7 +610,10 @@ cudaError_t launch_dc(const LaArgs& a, int dout, bool summary, bool exact, cudaS
         case 16: return launch_do<T, DC, 16>(a, summary, exact, s);
         case 32: return launch_do<T, DC, 32>(a, summary, exact, s);
         case 64: return launch_do<T, DC, 64>(a, summary, exact, s);
-        case 128: return launch_do<T, DC, 128>(a, summary, exact, s);
+        case 128:
+            // (bf16 heads of 128 x 128 run on tcgen05)
+            if constexpr (!(sizeof(T) == 2 && DC == 128))
+                return launch_do<T, DC, 128>(a, summary, exact, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -632,6 +635,7 @@ cudaError_t launch_type(const LaArgs& a, int dc, int dout, bool summary, bool ex
 cudaError_t launch_la_summary(const LaArgs& a, int dc, int dout, ckda_dtype dtype,
                               cudaStream_t s) {
     if (a.sp.units == 0) return cudaSuccess;
+    if (dtype == CKDA_BF16 && dc == 128 && dout == 128) return launch_la_tc_summary(a, s);
     return dtype == CKDA_BF16 ? launch_type<__nv_bfloat16>(a, dc, dout, true, false, s)
                               : launch_type<float>(a, dc, dout, true, false, s);
 }
@@ -639,6 +643,7 @@ cudaError_t launch_la_summary(const LaArgs& a, int dc, int dout, ckda_dtype dtyp
 cudaError_t launch_la_run(const LaArgs& a, int dc, int dout, bool exact, ckda_dtype dtype,
                           cudaStream_t s) {
     if (a.sp.units == 0) return cudaSuccess;
+    if (dtype == CKDA_BF16 && dc == 128 && dout == 128) return launch_la_tc_run(a, exact, s);
     return dtype == CKDA_BF16 ? launch_type<__nv_bfloat16>(a, dc, dout, false, exact, s)
                               : launch_type<float>(a, dc, dout, false, true, s);
 }

@@ -166,6 +166,13 @@ long long la_units(const int* cu_host, int n, int T, int L);
 // exact: operands that are formed in fp32 (decayed scores, states) enter the products in full
 // precision; otherwise rounded once to bf16 (bf16 inputs only).
 cudaError_t launch_la_summary(const LaArgs& a, int dc, int dout, ckda_dtype dtype, cudaStream_t s);
+// The same summaries and runs on the tcgen05 tensor cores: bf16, 128 x 128 heads (linattn_tc.cu).
+// A wait of theirs that runs out is kept as kLaStatusWait until la_status_take.
+constexpr int kLaStatusWait = 4;
+cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s);
+cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s);
+cudaError_t la_status_take(cudaStream_t stream, int* code);
+
 int la_scan_parts(int elems);    // partial sums of fin_dot per (sequence, head)
 cudaError_t launch_la_scan(const LaArgs& a, int dk, int dv, cudaStream_t s);
 // Final states of sequences without tokens (packed sequences in one unit each).

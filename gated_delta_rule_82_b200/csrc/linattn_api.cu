@@ -48,9 +48,8 @@ ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tok
     return CKDA_OK;
 }
 
-// Units that run side by side: two CTAs of the forward run fit an SM (148 SMs); of the backward's
-// one, with two or three runs sharing a launch.
-constexpr int kFwdSlots = 296, kBwdSlots = 148;
+// Units that run side by side: a CTA per SM.
+constexpr int kFwdSlots = 148, kBwdSlots = 148;
 
 LaSplit make_split(const Tokens& t, const int* cu, const int* cu_host, int H, int slots) {
     LaSplit sp;

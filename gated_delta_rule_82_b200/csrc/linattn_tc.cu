@@ -1,0 +1,745 @@
+// linattn_tc.cu -- chunked linear attention on the tcgen05 tensor cores (bf16, 128 x 128 heads).
+//
+// The runs of linattn.cuh for one unit of tokens per CTA, 64-token chunks, everything transposed
+// so that an output channel sits in a TMEM lane (M = 128) and 64 tokens in the columns:
+//     Sc  = X Y^T                        (64 x 64)    scores of the chunk
+//     O1^T = S^T X^T                     (128 x 64)   read-out of the entering state
+//     O2^T = Z^T P^T                     (128 x 64)   P: scores x decay, on the kept side
+//     U^T = (w Z)^T Y                    (128 x 128)  what the chunk adds to the state
+//     out_i = o exp(G_i) O1_i + O2_i,    S <- exp(G_C) S + U      (fp32, in registers)
+// X, Y, Z arrive by TMA as 128-byte-swizzled tiles; one tile serves as K-major and as MN-major
+// operand.  The state lives in the registers of eight warps (a row of 64 channels per thread) and
+// goes to the tensor core as a bf16 operand through TMEM; the weighted Z as well, in three bf16
+// terms (24 bits, a ring of four 32-column slots), so that states are fp32-grade.  With NP = 3 the
+// scores and the state enter in three terms too (the state's second and third from shared memory).
+//
+// Roles (one CTA per SM, all of TMEM): warps 0-3 weight Z; 4-11 carry the state; 12-15 turn
+// scores into P and write the outputs; then one warp each for TMA, tcgen05.mma and the decays.
+// They meet on mbarriers only, so a chunk's products overlap the neighbours' element work:
+// per chunk the tensor pipe needs 256 (Sc) + 768 (U) + 256 (O1) + 128 (O2) cycles at NP = 1.
+// Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
+// once its copies and products have landed.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "linattn.cuh"
+#include "tc_sm100.cuh"
+
+namespace ckda {
+
+namespace {
+
+constexpr int C = kLaChunk;
+constexpr int D = 128;                    // contracted and output channels
+constexpr int kTile = C * D * 2;          // bytes of one operand tile
+constexpr int kBlock = C * 128;           // 64 channels of it
+constexpr int kGateRing = 4, kWzRing = 4;
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// TMEM columns
+constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320, kColWz = 384;
+
+__device__ int g_la_status;               // 0, or kLaStatusWait since the host last read it
+
+struct TcArgs {
+    LaArgs a;
+    CUtensorMap map[kLaMaxRuns][3];       // x, y, z of every run
+};
+
+struct GateSlot {
+    float hi[C], lo[C], out[C], upd[C];
+    float total, pad[3];
+    double sum, pad2;
+};
+
+template <int NP, bool kSummary>
+struct TcShape {
+    static constexpr int STAGES = kSummary || NP == 1 ? 3 : 2;
+    static constexpr int STAGE = kSummary ? 2 * kTile : 3 * kTile;       // Y, Z, X
+    static constexpr int P = kSummary ? 0 : 2 * NP * kBlock;             // two buffers
+    static constexpr int SLO = kSummary ? 0 : (NP - 1) * D * D * 2;      // lower terms of the state
+    static constexpr int GATES = STAGES * STAGE + P + SLO;
+    static constexpr int DOT = GATES + kGateRing * (int)sizeof(GateSlot);
+    static constexpr int BARS = DOT + (kSummary ? 0 : 4 * C * 4);
+    static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
+    static constexpr int EXTRA = kSummary ? 12 : 16;                     // first of the single warps
+    static constexpr int THREADS = (EXTRA + 3) * 32;
+};
+
+struct Bars {
+    uint64_t full[3], empty[3], gfull[kGateRing], gempty[kGateRing];
+    uint64_t sc_full, sc_empty, p_full[2], p_empty[2], wz_full[kWzRing], wz_empty[kWzRing];
+    uint64_t u_full, u_empty, s_full, s_empty, o_full, o_empty, dot_full, dot_empty, fin_full, drain;
+    double fin[8];
+    uint32_t tmem;
+    volatile int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Whole-warp bounded wait; false once any wait of the CTA has run out.
+__device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
+    bool ok = true;
+    if (!tc::mbar_try_wait(bar, parity)) {
+        const unsigned long long t0 = now_ns();
+        for (uint32_t i = 0; !tc::mbar_try_wait(bar, parity); ++i) {
+            if (b.abort) { ok = false; break; }
+            if ((i & 63) == 63 && now_ns() - t0 > kWaitNs) { b.abort = 1; ok = false; break; }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low half
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15]) : "memory");
+}
+// 16 lanes x 64 columns spread over the warp: v[4 j + e] is row lane / 4 + 8 (e / 2), column
+// 8 j + 2 (lane % 4) + e % 2.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int NP, bool kSummary>
+__global__ void __launch_bounds__(TcShape<NP, kSummary>::THREADS, 1)
+la_tc_kernel(const __grid_constant__ TcArgs args) {
+    using S = TcShape<NP, kSummary>;
+    constexpr int NS = S::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sP = sm + NS * S::STAGE;
+    uint8_t* sSlo = sP + S::P;
+    GateSlot* gates = reinterpret_cast<GateSlot*>(sm + S::GATES);
+    float* sDot = reinterpret_cast<float*>(sm + S::DOT);
+    Bars& b = *reinterpret_cast<Bars*>(sm + S::BARS);
+
+    const LaArgs& a = args.a;
+    const LaRun& R = a.run[blockIdx.y];
+    const int H = a.sp.H, unit = blockIdx.x / H, h = blockIdx.x - unit * H;
+    const UnitAt u = find_unit(a.sp, unit);
+    if (!u.ok) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+    const bool rev = R.reverse;
+    const int n = (u.len + C - 1) / C;
+    auto chunk_at = [&](int i) { return rev ? n - 1 - i : i; };
+    auto live_of = [&](int i) { return min(C, u.len - chunk_at(i) * C); };
+
+    if (warp == S::EXTRA + 1) {
+        tc::tmem_alloc(&b.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(&b.full[i], 1);
+            tc::mbar_init(&b.empty[i], 5);            // the products, and the four warps that read Z
+        }
+        for (int i = 0; i < kGateRing; ++i) {
+            tc::mbar_init(&b.gfull[i], 1);
+            tc::mbar_init(&b.gempty[i], S::EXTRA);    // every element warp
+        }
+        for (int i = 0; i < kWzRing; ++i) {
+            tc::mbar_init(&b.wz_full[i], 4);
+            tc::mbar_init(&b.wz_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&b.p_full[i], 4);
+            tc::mbar_init(&b.p_empty[i], 1);
+        }
+        tc::mbar_init(&b.sc_full, 1);
+        tc::mbar_init(&b.sc_empty, 4);
+        tc::mbar_init(&b.u_full, 1);
+        tc::mbar_init(&b.u_empty, 8);
+        tc::mbar_init(&b.s_full, 8);
+        tc::mbar_init(&b.s_empty, 1);
+        tc::mbar_init(&b.o_full, 1);
+        tc::mbar_init(&b.o_empty, 4);
+        tc::mbar_init(&b.dot_full, 4);
+        tc::mbar_init(&b.dot_empty, 1);
+        tc::mbar_init(&b.fin_full, 8);
+        tc::mbar_init(&b.drain, 1);
+        b.abort = 0;
+        tc::fence_mbar_init();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = b.tmem;
+
+    if (warp < 4) {
+        // ------------------------------------------------ weighted Z: one output channel a thread
+        const int r = 32 * quarter + lane;
+        const uint32_t zoff = (r >> 6) * kBlock + (r & 7) * 2, zc = (r & 63) >> 3;
+        int term = 0;
+        for (int i = 0; i < n; ++i) {
+            const int st = i % NS, gs = i % kGateRing;
+            if (!wait(b, &b.full[st], (i / NS) & 1) || !wait(b, &b.gfull[gs], (i / kGateRing) & 1))
+                break;
+            const uint8_t* z = sm + st * S::STAGE + kTile + zoff;
+            const int live = live_of(i);
+            float v[C];
+#pragma unroll
+            for (int t = 0; t < C; ++t)
+                v[t] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(
+                                           z + t * 128 + ((zc ^ (t & 7)) << 4)) << 16);
+            arrive_warp(&b.empty[st]);
+            if (live < C) {                       // (rows behind the sequence's end are not its own)
+#pragma unroll
+                for (int t = 0; t < C; ++t) v[t] = t < live ? v[t] : 0.f;
+            }
+            const float4* w = reinterpret_cast<const float4*>(gates[gs].upd);
+#pragma unroll
+            for (int t = 0; t < C / 4; ++t) {
+                const float4 x = w[t];
+                v[4 * t] *= x.x; v[4 * t + 1] *= x.y; v[4 * t + 2] *= x.z; v[4 * t + 3] *= x.w;
+            }
+            arrive_warp(&b.gempty[gs]);
+            bool ok = true;
+            for (int k = 0; k < 3; ++k, ++term) {
+                const int slot = term % kWzRing;
+                if (term >= kWzRing && !wait(b, &b.wz_empty[slot], (term / kWzRing - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float& x0 = v[32 * q + 2 * j];
+                        float& x1 = v[32 * q + 2 * j + 1];
+                        p[j] = pack2(x0, x1);
+                        x0 -= lo_f(p[j]);
+                        x1 -= hi_f(p[j]);
+                    }
+                    tmem_st16(tc::tmem_addr(tmem, 32 * quarter, kColWz + 32 * slot + 16 * q), p);
+                }
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                arrive_warp(&b.wz_full[slot]);
+            }
+            if (!ok) break;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------ the state: 64 contracted channels of one row
+        const int row = 32 * quarter + lane, half = (warp - 4) >> 2, col0 = 64 * half;
+        const int rs = R.transposed ? D : 1, cs = R.transposed ? 1 : D;
+        const size_t seq_state = ((size_t)u.seq * H + h) * (D * D);
+        const size_t unit_state = ((size_t)unit * H + h) * (D * D);
+        const float* init = nullptr;
+        if (!kSummary) {
+            if (R.unit_state) init = R.unit_state + unit_state;
+            else if (R.init) init = R.init + seq_state;
+        }
+        float st[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            st[j] = init ? init[(size_t)row * rs + (size_t)(col0 + j) * cs] : 0.f;
+        double decay = 0.0;
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
+            const int gs = i % kGateRing;
+            if constexpr (!kSummary) {
+                if (i > 0 && !wait(b, &b.s_empty, (i - 1) & 1)) { ok = false; break; }
+                tc::tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[j] = pack2(st[32 * q + 2 * j], st[32 * q + 2 * j + 1]);
+                    tmem_st16(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half + 16 * q), p);
+                    if constexpr (NP > 1) {
+                        uint32_t m[16], l[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float x0 = st[32 * q + 2 * j] - lo_f(p[j]);
+                            const float x1 = st[32 * q + 2 * j + 1] - hi_f(p[j]);
+                            m[j] = pack2(x0, x1);
+                            l[j] = pack2(x0 - lo_f(m[j]), x1 - hi_f(m[j]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint8_t* at = sSlo + half * (D * 128) + row * 128 +
+                                          (((4 * q + j) ^ (row & 7)) << 4);
+                            *reinterpret_cast<uint4*>(at) =
+                                make_uint4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]);
+                            *reinterpret_cast<uint4*>(at + D * D * 2) =
+                                make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+                        }
+                    }
+                }
+                tc::tmem_st_wait();
+                if constexpr (NP > 1) tc::fence_proxy_async_smem();
+                tc::tc_fence_before();
+                arrive_warp(&b.s_full);
+            }
+            if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1)) { ok = false; break; }
+            const float total = gates[gs].total;
+            decay += gates[gs].sum;
+            arrive_warp(&b.gempty[gs]);
+            if (!wait(b, &b.u_full, i & 1)) { ok = false; break; }
+            tc::tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float x[16];
+                tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + col0 + 16 * q), x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) st[16 * q + j] = fmaf(st[16 * q + j], total, x[j]);
+            }
+            tc::tc_fence_before();
+            arrive_warp(&b.u_empty);
+        }
+        if (ok) {
+            float* fin = kSummary ? R.unit_state + unit_state
+                                  : (!R.unit_state && R.fin ? R.fin + seq_state : nullptr);
+            if (fin) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) fin[(size_t)row * rs + (size_t)(col0 + j) * cs] = st[j];
+            }
+            if (kSummary && warp == 4 && lane == 0) R.unit_decay[(size_t)unit * H + h] = decay;
+            if (!kSummary && !R.unit_state && R.fin_dot) {
+                const float* f = R.fin_dot + seq_state;
+                double d = 0.0;
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    d += (double)st[j] * (double)f[(size_t)row * rs + (size_t)(col0 + j) * cs];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                if (lane == 0) b.fin[warp - 4] = d;
+                arrive_warp(&b.fin_full);
+                if (warp == 4 && wait(b, &b.fin_full, 0) && lane == 0) {
+                    double s = 0.0;
+                    for (int w = 0; w < 8; ++w) s += b.fin[w];
+                    R.fin_dot_out[(size_t)u.seq * H + h] = s;
+                }
+            }
+        }
+    } else if (warp < S::EXTRA) {
+        // ------------------------------------------------------------ P from scores, and outputs
+        auto make_p = [&](int i) {
+            const int gs = i % kGateRing, buf = i & 1;
+            if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1) || !wait(b, &b.sc_full, i & 1)) return false;
+            tc::tc_fence_after();
+            float x[32];
+            tmem_ld_16x64(tc::tmem_addr(tmem, 32 * quarter, kColSc), x);
+            tc::tc_fence_before();
+            arrive_warp(&b.sc_empty);
+            if (i >= 2 && !wait(b, &b.p_empty[buf], (i / 2 - 1) & 1)) return false;
+            const GateSlot& g = gates[gs];
+            uint8_t* p = sP + buf * NP * kBlock;
+            const int r0 = 16 * quarter + (lane >> 2), c0 = 2 * (lane & 3), live = live_of(i);
+            const float h0 = g.hi[r0], l0 = g.lo[r0], h1 = g.hi[r0 + 8], l1 = g.lo[r0 + 8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = 8 * j + c0;
+                const float2 ch = *reinterpret_cast<const float2*>(g.hi + c);
+                const float2 cl = *reinterpret_cast<const float2*>(g.lo + c);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = r0 + 8 * e;
+                    const float rh = e ? h1 : h0, rl = e ? l1 : l0;
+                    float w0 = 0.f, w1 = 0.f;
+                    const float d0 = (rh - ch.x) + (rl - cl.x), d1 = (rh - ch.y) + (rl - cl.y);
+                    if (rev ? (row <= c && c < live) : row >= c)
+                        w0 = x[4 * j + 2 * e] * ex2(rev ? -d0 : d0) * R.p_scale;
+                    if (rev ? (row <= c + 1 && c + 1 < live) : row >= c + 1)
+                        w1 = x[4 * j + 2 * e + 1] * ex2(rev ? -d1 : d1) * R.p_scale;
+                    const uint32_t at = row * 128 + (((c >> 3) ^ (row & 7)) << 4) + (c & 7) * 2;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        const uint32_t t = pack2(w0, w1);
+                        *reinterpret_cast<uint32_t*>(p + q * kBlock + at) = t;
+                        w0 -= lo_f(t);
+                        w1 -= hi_f(t);
+                    }
+                }
+            }
+            tc::fence_proxy_async_smem();
+            arrive_warp(&b.p_full[buf]);
+            return true;
+        };
+        const int r = 32 * quarter + lane;                      // this thread's output channel
+        bool ok = make_p(0);
+        for (int i = 0; i < n && ok; ++i) {
+            if (i + 1 < n && !(ok = make_p(i + 1))) break;
+            const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i);
+            const long long tok = u.tok + (long long)c * C;
+            if (!(ok = wait(b, &b.o_full, i & 1))) break;
+            tc::tc_fence_after();
+            const size_t at = ((size_t)tok * H + h) * D + r, step = (size_t)H * D;
+            float dsum[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {                       // 32 tokens at a time
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x[16], y[16];
+                    tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColO1 + 32 * q + 16 * e), x);
+                    tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColO2 + 32 * q + 16 * e), y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[16 * e + j] =
+                            fmaf(x[j], gates[gs].out[32 * q + 16 * e + j] * R.o_scale, y[j]);
+                }
+                if (q == 1) {
+                    tc::tc_fence_before();
+                    arrive_warp(&b.o_empty);
+                }
+                if (R.out_f32) {
+                    float* dst = static_cast<float*>(R.out) + at + (size_t)(32 * q) * step;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (32 * q + j < live) dst[j * step] = o[j];
+                } else {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(R.out) + at + (size_t)(32 * q) * step;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (32 * q + j < live) dst[j * step] = __float2bfloat16_rn(o[j]);
+                }
+                if (R.dot) {
+                    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(R.dot) +
+                                             ((size_t)(tok + 32 * q) * (H / R.dg) + h / R.dg) * D + r;
+                    const size_t ws = (size_t)(H / R.dg) * D;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = 32 * q + j < live ? o[j] * __bfloat162float(w[j * ws]) : 0.f;
+                    // sum over the lanes, token j ending up in lane j
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1)
+#pragma unroll
+                        for (int j = 0; j < s; ++j) {
+                            const bool up = lane & s;
+                            const float send = up ? o[j] : o[j + s], keep = up ? o[j + s] : o[j];
+                            o[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+                        }
+                    dsum[q] = o[0];
+                }
+            }
+            arrive_warp(&b.gempty[gs]);
+            if (R.dot) {
+                if (i > 0 && !(ok = wait(b, &b.dot_empty, (i - 1) & 1))) break;
+                sDot[quarter * C + lane] = dsum[0];
+                sDot[quarter * C + 32 + lane] = dsum[1];
+                arrive_warp(&b.dot_full);
+                if (quarter == 0) {
+                    if (!(ok = wait(b, &b.dot_full, i & 1))) break;
+                    double sum = 0.0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = 32 * e + lane;
+                        const float s = (sDot[t] + sDot[C + t]) + (sDot[2 * C + t] + sDot[3 * C + t]);
+                        if (t < live) {
+                            R.dot_out[(size_t)(tok + t) * H + h] = s;
+                            sum += (double)s;
+                        }
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0)
+                        R.dot_sum[(size_t)la_chunk_id(u.tok - (long long)u.index * a.sp.L, u.seq,
+                                                      u.index * (a.sp.L / C) + c) * H + h] = sum;
+                    arrive_warp(&b.dot_empty);
+                }
+            }
+        }
+    } else if (warp == S::EXTRA) {
+        // ------------------------------------------------------------------------ TMA, one lane
+        const CUtensorMap* map = args.map[blockIdx.y];
+        const int hx = h / R.xg, hy = h / R.yg, hz = h / R.zg;
+        const int row = a.sp.cu ? 0 : u.seq;
+        const int tok0 = a.sp.cu ? (int)u.tok : u.index * a.sp.L;
+        int sent = 0;
+        if (lane == 0) {
+            for (int i = 0; i < n; ++i) {
+                const int st = i % NS;
+                if (i >= NS) {
+                    // (one lane: the wait's vote is the lane's own)
+                    const unsigned long long t0 = now_ns();
+                    bool ok = true;
+                    while (!tc::mbar_try_wait(&b.empty[st], (i / NS - 1) & 1)) {
+                        if (b.abort || now_ns() - t0 > kWaitNs) { b.abort = 1; ok = false; break; }
+                    }
+                    if (!ok) break;
+                }
+                uint8_t* dst = sm + st * S::STAGE;
+                const int t = tok0 + chunk_at(i) * C;
+                tc::mbar_arrive_expect_tx(&b.full[st], S::STAGE);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    tc::tma_load_4d(dst + k * kBlock, &map[1], 64 * k, hy, t, row, &b.full[st]);
+                    tc::tma_load_4d(dst + kTile + k * kBlock, &map[2], 64 * k, hz, t, row, &b.full[st]);
+                    if constexpr (!kSummary)
+                        tc::tma_load_4d(dst + 2 * kTile + k * kBlock, &map[0], 64 * k, hx, t, row,
+                                        &b.full[st]);
+                }
+                sent = i + 1;
+            }
+            // every copy has landed before the CTA leaves
+            for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) {
+                const unsigned long long t0 = now_ns();
+                while (!tc::mbar_try_wait(&b.full[i % NS], (i / NS) & 1) && now_ns() - t0 < kWaitNs) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp == S::EXTRA + 1) {
+        // -------------------------------------------------------------------------- tcgen05.mma
+        constexpr uint32_t id_sc = tc::idesc_bf16_f32(64, 64, 0, 0);
+        constexpr uint32_t id_o1 = tc::idesc_bf16_f32(128, 64, 0, 0);
+        constexpr uint32_t id_o2 = tc::idesc_bf16_f32(128, 64, 1, 0);
+        constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 128, 0, 1);
+        auto stage = [&](int i) { return tc::smem_u32(sm + (i % NS) * S::STAGE); };
+        auto scores = [&](int i) {
+            if (!wait(b, &b.full[i % NS], (i / NS) & 1)) return false;
+            if (a.sp.cu && live_of(i) < C) {
+                // packed: rows behind the sequence's end belong to the next one; they must not
+                // reach a product even as 0 x NaN
+                uint8_t* s = sm + (i % NS) * S::STAGE;
+                const int live = live_of(i), words = (C - live) * 8;     // 16-byte words per block
+                for (int k = 0; k < 2 * (S::STAGE / kTile); ++k)
+                    for (int w = lane; w < words; w += 32)
+                        *reinterpret_cast<uint4*>(s + k * kBlock + live * 128 + w * 16) =
+                            make_uint4(0, 0, 0, 0);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if constexpr (!kSummary) {
+                if (i > 0 && !wait(b, &b.sc_empty, (i - 1) & 1)) return false;
+                tc::tc_fence_after();
+                const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
+                const uint64_t yd = tc::smem_desc_sw128(stage(i), 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
+                    tc::mma_bf16_warp(tmem + kColSc, tc::desc_add(xd, off), tc::desc_add(yd, off),
+                                      id_sc, ks > 0);
+                }
+                tc::mma_commit_warp(&b.sc_full);
+            }
+            return true;
+        };
+        bool ok = scores(0);
+        int term = 0;
+        for (int i = 0; i < n && ok; ++i) {
+            // U: one term of the weighted Z after the other
+            if (i > 0 && !(ok = wait(b, &b.u_empty, (i - 1) & 1))) break;
+            const uint64_t yd = tc::smem_desc_sw128(stage(i), kBlock, 1024);
+            for (int k = 0; k < 3 && ok; ++k, ++term) {
+                const int slot = term % kWzRing;
+                if (!(ok = wait(b, &b.wz_full[slot], (term / kWzRing) & 1))) break;
+                tc::tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc::mma_bf16_tmem_a_warp(tmem + kColU, tmem + kColWz + 32 * slot + 8 * ks,
+                                             tc::desc_add(yd, ks * 2048), id_u, (k > 0 || ks > 0));
+                tc::mma_commit_warp(&b.wz_empty[slot]);
+            }
+            if (!ok) break;
+            tc::mma_commit_warp(&b.u_full);
+            if constexpr (kSummary) {
+                tc::mma_commit_warp(&b.empty[i % NS]);
+                if (i + 1 < n) ok = scores(i + 1);
+                continue;
+            }
+            if (i + 1 < n && !(ok = scores(i + 1))) break;
+            // O1: the entering state read by X
+            if (!(ok = wait(b, &b.s_full, i & 1))) break;
+            if (i > 0 && !(ok = wait(b, &b.o_empty, (i - 1) & 1))) break;
+            tc::tc_fence_after();
+            const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                tc::mma_bf16_tmem_a_warp(tmem + kColO1, tmem + kColS + 8 * ks,
+                                         tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1,
+                                         ks > 0);
+            if constexpr (NP > 1) {
+#pragma unroll
+                for (int q = 0; q < NP - 1; ++q) {
+                    const uint64_t sd = tc::smem_desc_sw128(tc::smem_u32(sSlo) + q * D * D * 2, 16, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc::mma_bf16_warp(tmem + kColO1,
+                                          tc::desc_add(sd, (ks >> 2) * (D * 128) + (ks & 3) * 32),
+                                          tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, 1);
+                }
+            }
+            tc::mma_commit_warp(&b.s_empty);
+            // O2: the chunk's own scores
+            const int buf = i & 1;
+            if (!(ok = wait(b, &b.p_full[buf], (i / 2) & 1))) break;
+            tc::tc_fence_after();
+            const uint64_t zd = tc::smem_desc_sw128(stage(i) + kTile, kBlock, 1024);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const uint64_t pd = tc::smem_desc_sw128(tc::smem_u32(sP) + (buf * NP + q) * kBlock, 16, 1024);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc::mma_bf16_warp(tmem + kColO2, tc::desc_add(zd, ks * 2048),
+                                      tc::desc_add(pd, ks * 32), id_o2, (q > 0 || ks > 0));
+            }
+            tc::mma_commit_warp(&b.p_empty[buf]);
+            tc::mma_commit_warp(&b.o_full);
+            tc::mma_commit_warp(&b.empty[i % NS]);
+        }
+        // every product has finished before the memory is given back
+        tc::mma_commit_warp(&b.drain);
+        const unsigned long long t0 = now_ns();
+        while (!tc::mbar_try_wait(&b.drain, 0) && now_ns() - t0 < kWaitNs) {}
+        __syncwarp();
+    } else {
+        // ----------------------------------------------------------------------------- decays
+        auto pair = [&](int i, double* g0, double* g1) {
+            const long long tok = u.tok + (long long)chunk_at(i) * C;
+            const int live = live_of(i);
+            *g0 = log2_decay(a.g, a.per_token, tok + 2 * lane, H, h, 2 * lane < live);
+            *g1 = log2_decay(a.g, a.per_token, tok + 2 * lane + 1, H, h, 2 * lane + 1 < live);
+        };
+        double g0, g1, n0 = 0.0, n1 = 0.0;
+        pair(0, &g0, &g1);
+        for (int i = 0; i < n; ++i) {
+            const int gs = i % kGateRing, live = live_of(i);
+            if (i + 1 < n) pair(i + 1, &n0, &n1);
+            double s = g0 + g1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += x;
+            }
+            const double all = __shfl_sync(0xffffffffu, s, 31);
+            const double G[2] = {s - g1, s};
+            if (i >= kGateRing && !wait(b, &b.gempty[gs], (i / kGateRing - 1) & 1)) break;
+            GateSlot& g = gates[gs];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                const float hi = (float)G[e], down = exp2f(hi), up = exp2f((float)(all - G[e]));
+                g.hi[t] = hi;
+                g.lo[t] = (float)(G[e] - (double)hi);
+                g.out[t] = rev ? up : down;
+                g.upd[t] = t < live ? (rev ? down : up) * R.u_scale : 0.f;
+            }
+            if (lane == 0) {
+                g.total = exp2f((float)all);
+                g.sum = all;
+            }
+            arrive_warp(&b.gfull[gs]);
+            g0 = n0;
+            g1 = n1;
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (b.abort && tid == 0) atomicCAS(&g_la_status, 0, kLaStatusWait);
+    if (warp == S::EXTRA + 1) tc::tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &qr) != cudaSuccess ||
+            qr != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// [rows][T][heads][128] bf16 as {channel, head, token, row}; boxes of 64 channels x 64 tokens of
+// one head.  Tokens behind T read as zeros.
+bool encode(CUtensorMap* m, const void* base, int heads, int T, int rows) {
+    auto enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)rows};
+    const cuuint64_t row = D * 2;
+    const cuuint64_t strides[3] = {row, row * heads, row * heads * T};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)C, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NP, bool kSummary>
+cudaError_t launch(const LaArgs& a, cudaStream_t s) {
+    using S = TcShape<NP, kSummary>;
+    TcArgs t;
+    t.a = a;
+    const int H = a.sp.H, rows = a.sp.cu ? 1 : a.sp.n;
+    for (int r = 0; r < a.runs; ++r) {
+        const LaRun& u = a.run[r];
+        if ((!kSummary && !encode(&t.map[r][0], u.x, H / u.xg, a.sp.T, rows)) ||
+            !encode(&t.map[r][1], u.y, H / u.yg, a.sp.T, rows) ||
+            !encode(&t.map[r][2], u.z, H / u.zg, a.sp.T, rows))
+            return cudaErrorInvalidValue;
+    }
+    auto kern = la_tc_kernel<NP, kSummary>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)(a.sp.units * H), a.runs), S::THREADS, S::SMEM, s>>>(t);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s) { return launch<1, true>(a, s); }
+cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s) {
+    return exact ? launch<3, false>(a, s) : launch<1, false>(a, s);
+}
+
+// Read this file's status word (`stream` has finished) and clear it.
+cudaError_t la_status_take(cudaStream_t stream, int* code) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_la_status, sizeof(int), 0,
+                                              cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && v != 0) {
+        static const int zero = 0;
+        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
+                                    stream);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    }
+    *code = v;
+    return e;
+}
+
+}  // namespace ckda
