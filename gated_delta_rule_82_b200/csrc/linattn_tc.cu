@@ -56,9 +56,11 @@ template <int NP, bool kSummary>
 struct TcShape {
     static constexpr int STAGES = kSummary || NP == 1 ? 3 : 2;
     static constexpr int STAGE = kSummary ? 2 * kTile : 3 * kTile;       // Y, Z, X
-    static constexpr int P = kSummary ? 0 : 2 * NP * kBlock;             // two buffers
+    static constexpr int PBUF = NP == 1 ? 2 : 1;                         // buffers of P
+    static constexpr int P = kSummary ? 0 : PBUF * NP * kBlock;
+    static constexpr int OUT = kSummary ? 0 : kTile;                     // outputs on their way out
     static constexpr int SLO = kSummary ? 0 : (NP - 1) * D * D * 2;      // lower terms of the state
-    static constexpr int GATES = STAGES * STAGE + P + SLO;
+    static constexpr int GATES = STAGES * STAGE + P + SLO + OUT;
     static constexpr int DOT = GATES + kGateRing * (int)sizeof(GateSlot);
     static constexpr int BARS = DOT + (kSummary ? 0 : 4 * C * 4);
     static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
@@ -81,17 +83,30 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
-// Whole-warp bounded wait; false once any wait of the CTA has run out.
-__device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
+// One poll that lets the warp sleep until the phase completes, or for about 20 us: polls without
+// a time hint return early, and the issue slots that waiting warps then take slow the working ones.
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
+    return ok != 0;
+}
+// Whole-warp bounded wait; false once any wait of the CTA has run out.  The loop is kept out of
+// line: the roles' code together has to stay in the instruction cache.
+__device__ __noinline__ bool wait_on(Bars* b, uint64_t* bar, uint32_t parity) {
     bool ok = true;
-    if (!tc::mbar_try_wait(bar, parity)) {
-        const unsigned long long t0 = now_ns();
-        for (uint32_t i = 0; !tc::mbar_try_wait(bar, parity); ++i) {
-            if (b.abort) { ok = false; break; }
-            if ((i & 63) == 63 && now_ns() - t0 > kWaitNs) { b.abort = 1; ok = false; break; }
-        }
+    const unsigned long long t0 = now_ns();
+    while (!poll(bar, parity)) {
+        if (b->abort) { ok = false; break; }
+        if (now_ns() - t0 > kWaitNs) { b->abort = 1; ok = false; break; }
     }
     return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, poll(bar, parity)) || wait_on(&b, bar, parity);
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
     __syncwarp();
@@ -110,31 +125,93 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* v) {
+// ---- two fp32 values at a time
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&r);
+}
+// The leading 8 bits of both values as a bf16 pair; x keeps the rest.  Cutting (not rounding)
+// leaves at most 16, then 8 significant bits, so three terms hold the 24 bits exactly.
+__device__ __forceinline__ uint32_t cut2(float2& x) {
+    const uint32_t a = __float_as_uint(x.x), b = __float_as_uint(x.y);
+    const uint32_t t = __byte_perm(a, b, 0x7632);
+    const float2 minus = make_float2(-1.f, -1.f);
+    x = fma2(make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)), minus, x);
+    return t;
+}
+
+// ---- TMEM in 16-lane pieces whose elements are spread over the warp like mma fragments
+// 16 lanes x 32 columns of packed bf16: v[2 j + e] is lane l / 4 + 8 e, column 4 j + l % 4.
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t* v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15, %16};"
         ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15]) : "memory");
 }
-// 16 lanes x 64 columns spread over the warp: v[4 j + e] is row lane / 4 + 8 (e / 2), column
-// 8 j + 2 (lane % 4) + e % 2.
-__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float* v) {
-    uint32_t r[32];
+// 16 lanes x 32 columns of fp32: v[2 j + e] holds lane l / 4 + 8 e, columns 8 j + 2 (l % 4) and
+// the one behind it.  No wait.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float2* v) {
+    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr) : "memory");
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+// A wait that the values depend on, so that no use of them is scheduled before it.
+__device__ __forceinline__ void ld_wait(float2* v, float2* w) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0].x), "+f"(v[0].y), "+f"(v[1].x), "+f"(v[1].y), "+f"(v[2].x), "+f"(v[2].y),
+                   "+f"(v[3].x), "+f"(v[3].y), "+f"(v[4].x), "+f"(v[4].y), "+f"(v[5].x), "+f"(v[5].y),
+                   "+f"(v[6].x), "+f"(v[6].y), "+f"(v[7].x), "+f"(v[7].y),
+                   "+f"(w[0].x), "+f"(w[0].y), "+f"(w[1].x), "+f"(w[1].y), "+f"(w[2].x), "+f"(w[2].y),
+                   "+f"(w[3].x), "+f"(w[3].y), "+f"(w[4].x), "+f"(w[4].y)
+                 :: "memory");
+    asm volatile("" : "+f"(w[5].x), "+f"(w[5].y), "+f"(w[6].x), "+f"(w[6].y), "+f"(w[7].x), "+f"(w[7].y));
+}
+// 16 lanes x 16 columns in the same layout; no wait.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float2* v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+__device__ __forceinline__ void tmem_ld_wait4(float2* v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0].x), "+f"(v[0].y), "+f"(v[1].x), "+f"(v[1].y), "+f"(v[2].x), "+f"(v[2].y),
+                   "+f"(v[3].x), "+f"(v[3].y)
+                 :: "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t r[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t a, const uint32_t r[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+                 :: "r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+// The output warps' staging: 64 tokens x 32 channels of bf16 per warp, 16-byte pieces swizzled so
+// that eight neighbouring tokens lie in different banks.
+__device__ __forceinline__ uint32_t stage_at(uint32_t tok, uint32_t piece) {
+    return tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4);
 }
 
 template <int NP, bool kSummary>
@@ -204,53 +281,59 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     const uint32_t tmem = b.tmem;
 
     if (warp < 4) {
-        // ------------------------------------------------ weighted Z: one output channel a thread
-        const int r = 32 * quarter + lane;
-        const uint32_t zoff = (r >> 6) * kBlock + (r & 7) * 2, zc = (r & 63) >> 3;
+        // ---------------------------------- weighted Z: 32 output channels a warp, 16 at a time.
+        // ldmatrix leaves the transposed tile in the layout that the 16-lane TMEM store takes.
+        const int m = lane >> 3;
+        const uint32_t zrow = ((m >> 1) * 8 + (lane & 7)) * 128 + (quarter >> 1) * kBlock;
+        const uint32_t zch = (quarter & 1) * 4 + (m & 1);        // 16-byte piece of the first half
         int term = 0;
         for (int i = 0; i < n; ++i) {
             const int st = i % NS, gs = i % kGateRing;
             if (!wait(b, &b.full[st], (i / NS) & 1) || !wait(b, &b.gfull[gs], (i / kGateRing) & 1))
                 break;
-            const uint8_t* z = sm + st * S::STAGE + kTile + zoff;
-            const int live = live_of(i);
-            float v[C];
+            const uint32_t z = tc::smem_u32(sm + st * S::STAGE + kTile) + zrow;
+            uint32_t p[2][16];                  // [half][4 tb + m]: tokens 16 tb + 8 (m / 2) ..
 #pragma unroll
-            for (int t = 0; t < C; ++t)
-                v[t] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(
-                                           z + t * 128 + ((zc ^ (t & 7)) << 4)) << 16);
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int tb = 0; tb < 4; ++tb)
+                    ldsm4t(&p[e][4 * tb], z + tb * 2048 + (((zch + 2 * e) ^ (lane & 7)) << 4));
             arrive_warp(&b.empty[st]);
-            if (live < C) {                       // (rows behind the sequence's end are not its own)
+            const int live = live_of(i);
+            if (live < C) {                     // (rows behind the sequence's end are not its own)
 #pragma unroll
-                for (int t = 0; t < C; ++t) v[t] = t < live ? v[t] : 0.f;
+                for (int j = 0; j < 16; ++j) {
+                    const int t = (j >> 2) * 16 + ((j >> 1) & 1) * 8 + 2 * (lane & 3);
+                    const uint32_t keep = t + 1 < live ? 0xffffffffu : t < live ? 0xffffu : 0u;
+                    p[0][j] &= keep;
+                    p[1][j] &= keep;
+                }
             }
-            const float4* w = reinterpret_cast<const float4*>(gates[gs].upd);
+            float2 v[2][16];
 #pragma unroll
-            for (int t = 0; t < C / 4; ++t) {
-                const float4 x = w[t];
-                v[4 * t] *= x.x; v[4 * t + 1] *= x.y; v[4 * t + 2] *= x.z; v[4 * t + 3] *= x.w;
+            for (int g = 0; g < 8; ++g) {       // 8 tokens
+                const float2 w = *reinterpret_cast<const float2*>(gates[gs].upd + 8 * g + 2 * (lane & 3));
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t x = p[e][2 * g + k];
+                        v[e][2 * g + k] = mul2(make_float2(lo_f(x), hi_f(x)), w);
+                    }
             }
             arrive_warp(&b.gempty[gs]);
             bool ok = true;
-            for (int k = 0; k < 3; ++k, ++term) {
+#pragma unroll 1
+            for (int k = 0; k < 3; ++k, ++term) {        // (one body: the third leaves zero)
                 const int slot = term % kWzRing;
-                if (term >= kWzRing && !wait(b, &b.wz_empty[slot], (term / kWzRing - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
+                if (term >= kWzRing && !(ok = wait(b, &b.wz_empty[slot], (term / kWzRing - 1) & 1))) break;
                 tc::tc_fence_after();
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t p[16];
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t t[16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float& x0 = v[32 * q + 2 * j];
-                        float& x1 = v[32 * q + 2 * j + 1];
-                        p[j] = pack2(x0, x1);
-                        x0 -= lo_f(p[j]);
-                        x1 -= hi_f(p[j]);
-                    }
-                    tmem_st16(tc::tmem_addr(tmem, 32 * quarter, kColWz + 32 * slot + 16 * q), p);
+                    for (int j = 0; j < 16; ++j) t[j] = cut2(v[e][j]);
+                    tmem_st_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColWz + 32 * slot), t);
                 }
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
@@ -264,65 +347,64 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const int rs = R.transposed ? D : 1, cs = R.transposed ? 1 : D;
         const size_t seq_state = ((size_t)u.seq * H + h) * (D * D);
         const size_t unit_state = ((size_t)unit * H + h) * (D * D);
+        const size_t own = (size_t)row * rs + (size_t)col0 * cs;
         const float* init = nullptr;
         if (!kSummary) {
             if (R.unit_state) init = R.unit_state + unit_state;
             else if (R.init) init = R.init + seq_state;
         }
-        float st[64];
+        float2 st[32];
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-            st[j] = init ? init[(size_t)row * rs + (size_t)(col0 + j) * cs] : 0.f;
+        for (int j = 0; j < 32; ++j)
+            st[j] = init ? make_float2(init[own + (size_t)(2 * j) * cs], init[own + (size_t)(2 * j + 1) * cs])
+                         : make_float2(0.f, 0.f);
         double decay = 0.0;
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
+        for (int i = 0; i < n; ++i) {
             const int gs = i % kGateRing;
             if constexpr (!kSummary) {
-                if (i > 0 && !wait(b, &b.s_empty, (i - 1) & 1)) { ok = false; break; }
+                if (i > 0 && !(ok = wait(b, &b.s_empty, (i - 1) & 1))) break;
                 tc::tc_fence_after();
+                uint32_t t[32];
+                if constexpr (NP == 1) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t p[16];
+                    for (int j = 0; j < 32; ++j) t[j] = pack2(st[j].x, st[j].y);
+                } else {
+                    // three terms: the first through TMEM, the others through shared memory
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) p[j] = pack2(st[32 * q + 2 * j], st[32 * q + 2 * j + 1]);
-                    tmem_st16(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half + 16 * q), p);
-                    if constexpr (NP > 1) {
-                        uint32_t m[16], l[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float x0 = st[32 * q + 2 * j] - lo_f(p[j]);
-                            const float x1 = st[32 * q + 2 * j + 1] - hi_f(p[j]);
-                            m[j] = pack2(x0, x1);
-                            l[j] = pack2(x0 - lo_f(m[j]), x1 - hi_f(m[j]));
-                        }
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t m[4], l[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            uint8_t* at = sSlo + half * (D * 128) + row * 128 +
-                                          (((4 * q + j) ^ (row & 7)) << 4);
-                            *reinterpret_cast<uint4*>(at) =
-                                make_uint4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]);
-                            *reinterpret_cast<uint4*>(at + D * D * 2) =
-                                make_uint4(l[4 * j], l[4 * j + 1], l[4 * j + 2], l[4 * j + 3]);
+                            float2 x = st[4 * q + j];
+                            t[4 * q + j] = cut2(x);
+                            m[j] = cut2(x);
+                            l[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
                         }
+                        uint8_t* at = sSlo + half * (D * 128) + row * 128 + ((q ^ (row & 7)) << 4);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(m[0], m[1], m[2], m[3]);
+                        *reinterpret_cast<uint4*>(at + D * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
                     }
                 }
+                tc::tmem_st32(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half), t);
                 tc::tmem_st_wait();
                 if constexpr (NP > 1) tc::fence_proxy_async_smem();
                 tc::tc_fence_before();
                 arrive_warp(&b.s_full);
             }
-            if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1)) { ok = false; break; }
-            const float total = gates[gs].total;
-            decay += gates[gs].sum;
+            if (!(ok = wait(b, &b.gfull[gs], (i / kGateRing) & 1))) break;
+            const float2 total = make_float2(gates[gs].total, gates[gs].total);
+            if constexpr (kSummary) decay += gates[gs].sum;
             arrive_warp(&b.gempty[gs]);
-            if (!wait(b, &b.u_full, i & 1)) { ok = false; break; }
+            if (!(ok = wait(b, &b.u_full, i & 1))) break;
             tc::tc_fence_after();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float x[16];
-                tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + col0 + 16 * q), x);
+            for (int q = 0; q < 2; ++q) {
+                float x[32];
+                tc::tmem_ld32_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + col0 + 32 * q), x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) st[16 * q + j] = fmaf(st[16 * q + j], total, x[j]);
+                for (int j = 0; j < 16; ++j)
+                    st[16 * q + j] = fma2(st[16 * q + j], total, make_float2(x[2 * j], x[2 * j + 1]));
             }
             tc::tc_fence_before();
             arrive_warp(&b.u_empty);
@@ -332,15 +414,19 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                                   : (!R.unit_state && R.fin ? R.fin + seq_state : nullptr);
             if (fin) {
 #pragma unroll
-                for (int j = 0; j < 64; ++j) fin[(size_t)row * rs + (size_t)(col0 + j) * cs] = st[j];
+                for (int j = 0; j < 32; ++j) {
+                    fin[own + (size_t)(2 * j) * cs] = st[j].x;
+                    fin[own + (size_t)(2 * j + 1) * cs] = st[j].y;
+                }
             }
             if (kSummary && warp == 4 && lane == 0) R.unit_decay[(size_t)unit * H + h] = decay;
             if (!kSummary && !R.unit_state && R.fin_dot) {
-                const float* f = R.fin_dot + seq_state;
+                const float* f = R.fin_dot + seq_state + own;
                 double d = 0.0;
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    d += (double)st[j] * (double)f[(size_t)row * rs + (size_t)(col0 + j) * cs];
+                for (int j = 0; j < 32; ++j)
+                    d += (double)st[j].x * (double)f[(size_t)(2 * j) * cs] +
+                         (double)st[j].y * (double)f[(size_t)(2 * j + 1) * cs];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
                 if (lane == 0) b.fin[warp - 4] = d;
@@ -354,110 +440,207 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         }
     } else if (warp < S::EXTRA) {
         // ------------------------------------------------------------ P from scores, and outputs
-        auto make_p = [&](int i) {
-            const int gs = i % kGateRing, buf = i & 1;
-            if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1) || !wait(b, &b.sc_full, i & 1)) return false;
-            tc::tc_fence_after();
-            float x[32];
-            tmem_ld_16x64(tc::tmem_addr(tmem, 32 * quarter, kColSc), x);
-            tc::tc_fence_before();
-            arrive_warp(&b.sc_empty);
-            if (i >= 2 && !wait(b, &b.p_empty[buf], (i / 2 - 1) & 1)) return false;
-            const GateSlot& g = gates[gs];
-            uint8_t* p = sP + buf * NP * kBlock;
-            const int r0 = 16 * quarter + (lane >> 2), c0 = 2 * (lane & 3), live = live_of(i);
-            const float h0 = g.hi[r0], l0 = g.lo[r0], h1 = g.hi[r0 + 8], l1 = g.lo[r0 + 8];
+        constexpr int PB = S::PBUF;
+        const int gr = lane >> 2, gc = 2 * (lane & 3);
+        const float p_scale = R.p_scale, o_scale = R.o_scale;
+        uint8_t* sOut = sSlo + S::SLO + (warp - 12) * (kTile / 4);
+        // P is zero beyond the diagonal: those 16 x 8 tiles are cleared once and stay
+        for (int k = 0; k < PB * NP; ++k)
+            for (int w = lane; w < 16 * 8; w += 32) {
+                const int row = 16 * quarter + (w >> 3), c8 = w & 7;
+                if (rev ? c8 < 2 * quarter : c8 > 2 * quarter + 1)
+                    *reinterpret_cast<uint4*>(sP + k * kBlock + row * 128 + ((c8 ^ (row & 7)) << 4)) =
+                        make_uint4(0, 0, 0, 0);
+            }
+        // 16 x 16 tiles: 16 tokens (this warp's rows) against the 16 tokens from c0
+        auto put = [&](uint8_t* p, int c0, float2 w[4]) {     // w[2 j + e]: columns 8 j, rows 8 e
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = 8 * j + c0;
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t at = ((((uint32_t)c0 >> 3) + j) ^ gr) << 4;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        *reinterpret_cast<uint32_t*>(p + q * kBlock + e * 1024 + at) =
+                            NP == 1 ? pack2(w[2 * j + e].x, w[2 * j + e].y) : cut2(w[2 * j + e]);
+            }
+        };
+        auto make_p = [&](int i) {
+            const int gs = i % kGateRing, buf = i % PB;
+            if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1)) return false;
+            const GateSlot& g = gates[gs];
+            const int r0 = 16 * quarter + gr;
+            const float rh[2] = {g.hi[r0], g.hi[r0 + 8]}, rl[2] = {g.lo[r0], g.lo[r0 + 8]};
+            // Tiles off the diagonal: the decay between row and column passes the edge of this
+            // warp's 16 rows, exp(G_i - G_j) = exp(G_i - edge) exp(edge - G_j), both at most one.
+            const int edge = rev ? 16 * quarter + 15 : 16 * quarter - 1;
+            const float eh = edge >= 0 ? g.hi[edge] : 0.f, el = edge >= 0 ? g.lo[edge] : 0.f;
+            const float sg = rev ? -1.f : 1.f;
+            float ra[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) ra[e] = ex2(sg * ((rh[e] - eh) + (rl[e] - el))) * p_scale;
+            if (!wait(b, &b.sc_full, i & 1)) return false;
+            if (i >= PB && !wait(b, &b.p_empty[buf], (i / PB - 1) & 1)) return false;
+            tc::tc_fence_after();
+            const uint32_t sc = tc::tmem_addr(tmem, 32 * quarter, kColSc);
+            uint8_t* p = sP + buf * NP * kBlock + r0 * 128 + gc * 2;
+            float2 x[4], nx[4];
+            tmem_ld_16x16(sc + 16 * quarter, x);
+            // the diagonal tile, while the first of the others is on its way
+            int t = rev ? 3 : 0;
+            const int dt = rev ? -1 : 1;
+            tmem_ld_wait4(x);
+            if (t != quarter) tmem_ld_16x16(sc + 16 * t, nx);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = 16 * quarter + 8 * j + gc;
                 const float2 ch = *reinterpret_cast<const float2*>(g.hi + c);
                 const float2 cl = *reinterpret_cast<const float2*>(g.lo + c);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = r0 + 8 * e;
-                    const float rh = e ? h1 : h0, rl = e ? l1 : l0;
-                    float w0 = 0.f, w1 = 0.f;
-                    const float d0 = (rh - ch.x) + (rl - cl.x), d1 = (rh - ch.y) + (rl - cl.y);
-                    if (rev ? (row <= c && c < live) : row >= c)
-                        w0 = x[4 * j + 2 * e] * ex2(rev ? -d0 : d0) * R.p_scale;
-                    if (rev ? (row <= c + 1 && c + 1 < live) : row >= c + 1)
-                        w1 = x[4 * j + 2 * e + 1] * ex2(rev ? -d1 : d1) * R.p_scale;
-                    const uint32_t at = row * 128 + (((c >> 3) ^ (row & 7)) << 4) + (c & 7) * 2;
-#pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        const uint32_t t = pack2(w0, w1);
-                        *reinterpret_cast<uint32_t*>(p + q * kBlock + at) = t;
-                        w0 -= lo_f(t);
-                        w1 -= hi_f(t);
-                    }
+                    const float d0 = (rh[e] - ch.x) + (rl[e] - cl.x), d1 = (rh[e] - ch.y) + (rl[e] - cl.y);
+                    float2& w = x[2 * j + e];
+                    w.x = (rev ? row <= c : row >= c) ? w.x * ex2(sg * d0) * p_scale : 0.f;
+                    w.y = (rev ? row <= c + 1 : row >= c + 1) ? w.y * ex2(sg * d1) * p_scale : 0.f;
                 }
             }
+            put(p, 16 * quarter, x);
+#pragma unroll 1
+            for (; t != quarter; t += dt) {
+                tmem_ld_wait4(nx);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = nx[j];
+                if (t + dt != quarter) tmem_ld_16x16(sc + 16 * (t + dt), nx);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = 16 * t + 8 * j + gc;
+                    const float2 ch = *reinterpret_cast<const float2*>(g.hi + c);
+                    const float2 cl = *reinterpret_cast<const float2*>(g.lo + c);
+                    const float2 cb = make_float2(ex2(sg * ((eh - ch.x) + (el - cl.x))),
+                                                  ex2(sg * ((eh - ch.y) + (el - cl.y))));
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        x[2 * j + e] = mul2(mul2(x[2 * j + e], cb), make_float2(ra[e], ra[e]));
+                }
+                put(p, 16 * t, x);
+            }
+            tc::tc_fence_before();
+            arrive_warp(&b.sc_empty);
             tc::fence_proxy_async_smem();
             arrive_warp(&b.p_full[buf]);
             return true;
         };
-        const int r = 32 * quarter + lane;                      // this thread's output channel
+        const int ch0 = 32 * quarter;                            // this warp's output channels
+        const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
+        const int m = lane >> 3;                                 // matrix of an x4 access
+        const bool dots = R.dot != nullptr, out_f32 = R.out_f32;
         bool ok = make_p(0);
         for (int i = 0; i < n && ok; ++i) {
             if (i + 1 < n && !(ok = make_p(i + 1))) break;
             const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i);
             const long long tok = u.tok + (long long)c * C;
+            if (dots) {
+                // the rows that the outputs are multiplied with, into the staging area
+                const int Hd = H / R.dg;
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.dot) +
+                                           ((size_t)tok * Hd + h / R.dg) * D + ch0 + 8 * tp;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int t = 8 * k + tr;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (t < live) w = __ldg(reinterpret_cast<const uint4*>(src + (size_t)t * Hd * D));
+                    *reinterpret_cast<uint4*>(sOut + stage_at(t, tp)) = w;
+                }
+                __syncwarp();
+            }
             if (!(ok = wait(b, &b.o_full, i & 1))) break;
             tc::tc_fence_after();
-            const size_t at = ((size_t)tok * H + h) * D + r, step = (size_t)H * D;
-            float dsum[2];
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {                        // 32 tokens
+                float2 w[4], dot[4];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {                       // 32 tokens at a time
-                float o[32];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x[16], y[16];
-                    tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColO1 + 32 * q + 16 * e), x);
-                    tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColO2 + 32 * q + 16 * e), y);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        o[16 * e + j] =
-                            fmaf(x[j], gates[gs].out[32 * q + 16 * e + j] * R.o_scale, y[j]);
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = *reinterpret_cast<const float2*>(gates[gs].out + 32 * q + 8 * j + gc);
+                    w[j].x *= o_scale;
+                    w[j].y *= o_scale;
+                    dot[j] = make_float2(0.f, 0.f);
                 }
-                if (q == 1) {
-                    tc::tc_fence_before();
-                    arrive_warp(&b.o_empty);
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {                    // 16 channels
+                    float2 x[8], y[8];
+                    tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO1 + 32 * q), x);
+                    tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO2 + 32 * q), y);
+                    ld_wait(x, y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = fma2(x[j], w[j >> 1], y[j]);
+                    if (dots) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {            // 16 tokens: four 8 x 8 matrices
+                            uint32_t d[4];
+                            ldsm4t(d, tc::smem_u32(sOut) +
+                                          stage_at(32 * q + 16 * j + 8 * (m >> 1) + (lane & 7), 2 * e + (m & 1)));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                dot[2 * j + (k >> 1)] = fma2(x[4 * j + k], make_float2(lo_f(d[k]), hi_f(d[k])),
+                                                             dot[2 * j + (k >> 1)]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!out_f32) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[k] = pack2(x[4 * j + k].x, x[4 * j + k].y);
+                            stsm4t(tc::smem_u32(sOut) +
+                                       stage_at(32 * q + 16 * j + 8 * (m >> 1) + (lane & 7), 2 * e + (m & 1)), o);
+                        }
+                    } else {
+                        float* dst = static_cast<float*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 16 * e + gr;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int t = 32 * q + 8 * (j >> 1) + gc;
+                            float* at = dst + (size_t)t * H * D + 8 * (j & 1);
+                            if (t < live) at[0] = x[j].x;
+                            if (t + 1 < live) at[(size_t)H * D] = x[j].y;
+                        }
+                    }
                 }
-                if (R.out_f32) {
-                    float* dst = static_cast<float*>(R.out) + at + (size_t)(32 * q) * step;
+                if (dots) {
+                    if (q == 0 && i > 0 && !(ok = wait(b, &b.dot_empty, (i - 1) & 1))) break;
+                    // sum over the lanes that hold other channels
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * q + j < live) dst[j * step] = o[j];
-                } else {
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(R.out) + at + (size_t)(32 * q) * step;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * q + j < live) dst[j * step] = __float2bfloat16_rn(o[j]);
-                }
-                if (R.dot) {
-                    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(R.dot) +
-                                             ((size_t)(tok + 32 * q) * (H / R.dg) + h / R.dg) * D + r;
-                    const size_t ws = (size_t)(H / R.dg) * D;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] = 32 * q + j < live ? o[j] * __bfloat162float(w[j * ws]) : 0.f;
-                    // sum over the lanes, token j ending up in lane j
-#pragma unroll
-                    for (int s = 16; s > 0; s >>= 1)
+                    for (int s = 2; s > 0; s >>= 1)
 #pragma unroll
                         for (int j = 0; j < s; ++j) {
-                            const bool up = lane & s;
-                            const float send = up ? o[j] : o[j + s], keep = up ? o[j + s] : o[j];
-                            o[j] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+                            const bool up = lane & (8 * s);
+                            const float2 send = up ? dot[j] : dot[j + s], keep = up ? dot[j + s] : dot[j];
+                            dot[j].x = keep.x + __shfl_xor_sync(0xffffffffu, send.x, 8 * s);
+                            dot[j].y = keep.y + __shfl_xor_sync(0xffffffffu, send.y, 8 * s);
                         }
-                    dsum[q] = o[0];
+                    dot[0].x += __shfl_xor_sync(0xffffffffu, dot[0].x, 4);
+                    dot[0].y += __shfl_xor_sync(0xffffffffu, dot[0].y, 4);
+                    if (!(lane & 4))
+                        *reinterpret_cast<float2*>(sDot + quarter * C + 32 * q + 8 * (lane >> 3) + gc) = dot[0];
                 }
             }
+            if (!ok) break;
+            tc::tc_fence_before();
+            arrive_warp(&b.o_empty);
             arrive_warp(&b.gempty[gs]);
-            if (R.dot) {
-                if (i > 0 && !(ok = wait(b, &b.dot_empty, (i - 1) & 1))) break;
-                sDot[quarter * C + lane] = dsum[0];
-                sDot[quarter * C + 32 + lane] = dsum[1];
+            if (!out_f32) {
+                __syncwarp();
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 8 * tp;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int t = 8 * k + tr;
+                    const uint4 w = *reinterpret_cast<const uint4*>(sOut + stage_at(t, tp));
+                    if (t < live) *reinterpret_cast<uint4*>(dst + (size_t)t * H * D) = w;
+                }
+                __syncwarp();
+            }
+            if (dots) {
                 arrive_warp(&b.dot_full);
                 if (quarter == 0) {
                     if (!(ok = wait(b, &b.dot_full, i & 1))) break;
@@ -490,11 +673,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         if (lane == 0) {
             for (int i = 0; i < n; ++i) {
                 const int st = i % NS;
-                if (i >= NS) {
-                    // (one lane: the wait's vote is the lane's own)
+                if (i >= NS) {            // (one lane: no vote)
                     const unsigned long long t0 = now_ns();
                     bool ok = true;
-                    while (!tc::mbar_try_wait(&b.empty[st], (i / NS - 1) & 1)) {
+                    while (!poll(&b.empty[st], (i / NS - 1) & 1)) {
                         if (b.abort || now_ns() - t0 > kWaitNs) { b.abort = 1; ok = false; break; }
                     }
                     if (!ok) break;
@@ -515,7 +697,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             // every copy has landed before the CTA leaves
             for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) {
                 const unsigned long long t0 = now_ns();
-                while (!tc::mbar_try_wait(&b.full[i % NS], (i / NS) & 1) && now_ns() - t0 < kWaitNs) {}
+                while (!poll(&b.full[i % NS], (i / NS) & 1) && now_ns() - t0 < kWaitNs) {}
             }
         }
         __syncwarp();
@@ -545,7 +727,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 tc::tc_fence_after();
                 const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
                 const uint64_t yd = tc::smem_desc_sw128(stage(i), 16, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 8; ++ks) {
                     const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
                     tc::mma_bf16_warp(tmem + kColSc, tc::desc_add(xd, off), tc::desc_add(yd, off),
@@ -565,7 +747,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 const int slot = term % kWzRing;
                 if (!(ok = wait(b, &b.wz_full[slot], (term / kWzRing) & 1))) break;
                 tc::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 4; ++ks)
                     tc::mma_bf16_tmem_a_warp(tmem + kColU, tmem + kColWz + 32 * slot + 8 * ks,
                                              tc::desc_add(yd, ks * 2048), id_u, (k > 0 || ks > 0));
@@ -584,16 +766,16 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (i > 0 && !(ok = wait(b, &b.o_empty, (i - 1) & 1))) break;
             tc::tc_fence_after();
             const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < 8; ++ks)
                 tc::mma_bf16_tmem_a_warp(tmem + kColO1, tmem + kColS + 8 * ks,
                                          tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1,
                                          ks > 0);
             if constexpr (NP > 1) {
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < NP - 1; ++q) {
                     const uint64_t sd = tc::smem_desc_sw128(tc::smem_u32(sSlo) + q * D * D * 2, 16, 1024);
-#pragma unroll
+#pragma unroll 1
                     for (int ks = 0; ks < 8; ++ks)
                         tc::mma_bf16_warp(tmem + kColO1,
                                           tc::desc_add(sd, (ks >> 2) * (D * 128) + (ks & 3) * 32),
@@ -602,14 +784,14 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
             tc::mma_commit_warp(&b.s_empty);
             // O2: the chunk's own scores
-            const int buf = i & 1;
-            if (!(ok = wait(b, &b.p_full[buf], (i / 2) & 1))) break;
+            const int buf = i % S::PBUF;
+            if (!(ok = wait(b, &b.p_full[buf], (i / S::PBUF) & 1))) break;
             tc::tc_fence_after();
             const uint64_t zd = tc::smem_desc_sw128(stage(i) + kTile, kBlock, 1024);
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < NP; ++q) {
                 const uint64_t pd = tc::smem_desc_sw128(tc::smem_u32(sP) + (buf * NP + q) * kBlock, 16, 1024);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 4; ++ks)
                     tc::mma_bf16_warp(tmem + kColO2, tc::desc_add(zd, ks * 2048),
                                       tc::desc_add(pd, ks * 32), id_o2, (q > 0 || ks > 0));
@@ -621,7 +803,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         // every product has finished before the memory is given back
         tc::mma_commit_warp(&b.drain);
         const unsigned long long t0 = now_ns();
-        while (!tc::mbar_try_wait(&b.drain, 0) && now_ns() - t0 < kWaitNs) {}
+        while (!poll(&b.drain, 0) && now_ns() - t0 < kWaitNs) {}
         __syncwarp();
     } else {
         // ----------------------------------------------------------------------------- decays
