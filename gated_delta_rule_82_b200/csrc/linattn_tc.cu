@@ -14,8 +14,9 @@
 // scores and the state enter in three terms too (the state's second and third from shared memory).
 //
 // Roles (one CTA per SM, all of TMEM): warps 0-3 weight Z; 4-11 carry the state; 12-15 turn
-// scores into P and write the outputs; then one warp each for TMA, tcgen05.mma and the decays.
-// They meet on mbarriers only, so a chunk's products overlap the neighbours' element work:
+// scores into P and write the outputs; then one warp each for TMA and the decays, the products U,
+// the products Sc, and O1 with O2 (a poll of a barrier takes 80 cycles even when it is complete, so one
+// warp that issued all of them would be the slowest part).  They meet on mbarriers only, so a chunk's products overlap the neighbours' element work:
 // per chunk the tensor pipe needs 256 (Sc) + 768 (U) + 256 (O1) + 128 (O2) cycles at NP = 1.
 // Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
 // once its copies and products have landed.
@@ -44,6 +45,7 @@ __device__ int g_la_status;               // 0, or kLaStatusWait since the host 
 struct TcArgs {
     LaArgs a;
     CUtensorMap map[kLaMaxRuns][3];       // x, y, z of every run
+    CUtensorMap out[kLaMaxRuns];          // bf16 outputs
 };
 
 struct GateSlot {
@@ -65,13 +67,13 @@ struct TcShape {
     static constexpr int BARS = DOT + (kSummary ? 0 : 4 * C * 4);
     static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
     static constexpr int EXTRA = kSummary ? 12 : 16;                     // first of the single warps
-    static constexpr int THREADS = (EXTRA + 3) * 32;
+    static constexpr int THREADS = (EXTRA + (kSummary ? 2 : 4)) * 32;    // (20 warps: 96 registers each)
 };
 
 struct Bars {
     uint64_t full[3], empty[3], gfull[kGateRing], gempty[kGateRing];
     uint64_t sc_full, sc_empty, p_full[2], p_empty[2], wz_full[kWzRing], wz_empty[kWzRing];
-    uint64_t u_full, u_empty, s_full, s_empty, o_full, o_empty, dot_full, dot_empty, fin_full, drain;
+    uint64_t u_full, u_empty, s_full, s_empty, o_full, o_empty, dot_full, dot_empty, fin_full, tail, drain[3];
     double fin[8];
     uint32_t tmem;
     volatile int abort;
@@ -106,7 +108,7 @@ __device__ __noinline__ bool wait_on(Bars* b, uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, poll(bar, parity)) || wait_on(&b, bar, parity);
+    return __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)) || wait_on(&b, bar, parity);
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
     __syncwarp();
@@ -124,6 +126,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low 
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// One lane of a converged warp.  A group of products issued by it in one unrolled run keeps the
+// tensor pipe fed (34 cycles per 128 x 64 x 16, 66 per 128 x 128 x 16); a loop of single products
+// takes 77 cycles each whatever their size, and twice that beside busy warps.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
 
 // ---- two fp32 values at a time
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -158,6 +175,12 @@ __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t* v)
         ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15]) : "memory");
+}
+// 32 lanes x 8 columns, a lane per thread.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+                 "r"(v[6]), "r"(v[7]) : "memory");
 }
 // 16 lanes x 32 columns of fp32: v[2 j + e] holds lane l / 4 + 8 e, columns 8 j + 2 (l % 4) and
 // the one behind it.  No wait.
@@ -246,7 +269,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&b.full[i], 1);
-            tc::mbar_init(&b.empty[i], 5);            // the products, and the four warps that read Z
+            tc::mbar_init(&b.empty[i], kSummary ? 5 : 7);   // the products; four warps that read Z
         }
         for (int i = 0; i < kGateRing; ++i) {
             tc::mbar_init(&b.gfull[i], 1);
@@ -271,7 +294,8 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         tc::mbar_init(&b.dot_full, 4);
         tc::mbar_init(&b.dot_empty, 1);
         tc::mbar_init(&b.fin_full, 8);
-        tc::mbar_init(&b.drain, 1);
+        tc::mbar_init(&b.tail, 1);
+        for (int i = 0; i < 3; ++i) tc::mbar_init(&b.drain[i], 1);
         b.abort = 0;
         tc::fence_mbar_init();
     }
@@ -365,28 +389,31 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if constexpr (!kSummary) {
                 if (i > 0 && !(ok = wait(b, &b.s_empty, (i - 1) & 1))) break;
                 tc::tc_fence_after();
-                uint32_t t[32];
-                if constexpr (NP == 1) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) t[j] = pack2(st[j].x, st[j].y);
-                } else {
-                    // three terms: the first through TMEM, the others through shared memory
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t t[8];
+                    if constexpr (NP == 1) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        uint32_t m[4], l[4];
+                        for (int j = 0; j < 8; ++j) t[j] = pack2(st[8 * k + j].x, st[8 * k + j].y);
+                    } else {
+                        // three terms: the first through TMEM, the others through shared memory
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float2 x = st[4 * q + j];
-                            t[4 * q + j] = cut2(x);
-                            m[j] = cut2(x);
-                            l[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t m[4], l[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float2 x = st[8 * k + 4 * q + j];
+                                t[4 * q + j] = cut2(x);
+                                m[j] = cut2(x);
+                                l[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+                            }
+                            uint8_t* at = sSlo + half * (D * 128) + row * 128 + (((2 * k + q) ^ (row & 7)) << 4);
+                            *reinterpret_cast<uint4*>(at) = make_uint4(m[0], m[1], m[2], m[3]);
+                            *reinterpret_cast<uint4*>(at + D * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
                         }
-                        uint8_t* at = sSlo + half * (D * 128) + row * 128 + ((q ^ (row & 7)) << 4);
-                        *reinterpret_cast<uint4*>(at) = make_uint4(m[0], m[1], m[2], m[3]);
-                        *reinterpret_cast<uint4*>(at + D * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
                     }
+                    tmem_st8(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half + 8 * k), t);
                 }
-                tc::tmem_st32(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half), t);
                 tc::tmem_st_wait();
                 if constexpr (NP > 1) tc::fence_proxy_async_smem();
                 tc::tc_fence_before();
@@ -399,12 +426,12 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (!(ok = wait(b, &b.u_full, i & 1))) break;
             tc::tc_fence_after();
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float x[32];
-                tc::tmem_ld32_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + col0 + 32 * q), x);
+            for (int q = 0; q < 4; ++q) {
+                float x[16];
+                tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + col0 + 16 * q), x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    st[16 * q + j] = fma2(st[16 * q + j], total, make_float2(x[2 * j], x[2 * j + 1]));
+                for (int j = 0; j < 8; ++j)
+                    st[8 * q + j] = fma2(st[8 * q + j], total, make_float2(x[2 * j], x[2 * j + 1]));
             }
             tc::tc_fence_before();
             arrive_warp(&b.u_empty);
@@ -535,11 +562,14 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
         const int m = lane >> 3;                                 // matrix of an x4 access
         const bool dots = R.dot != nullptr, out_f32 = R.out_f32;
+        const int row_b = a.sp.cu ? 0 : u.seq, row0 = a.sp.cu ? (int)u.tok : u.index * a.sp.L;
         bool ok = make_p(0);
         for (int i = 0; i < n && ok; ++i) {
             if (i + 1 < n && !(ok = make_p(i + 1))) break;
             const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i);
             const long long tok = u.tok + (long long)c * C;
+            if (lane == 0) tc::bulk_wait_read_all();             // the staging area is free again
+            __syncwarp();
             if (dots) {
                 // the rows that the outputs are multiplied with, into the staging area
                 const int Hd = H / R.dg;
@@ -630,15 +660,21 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             arrive_warp(&b.o_empty);
             arrive_warp(&b.gempty[gs]);
             if (!out_f32) {
-                __syncwarp();
-                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 8 * tp;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int t = 8 * k + tr;
-                    const uint4 w = *reinterpret_cast<const uint4*>(sOut + stage_at(t, tp));
-                    if (t < live) *reinterpret_cast<uint4*>(dst + (size_t)t * H * D) = w;
+                if (a.sp.cu && live < C) {        // (the rows behind are another sequence's)
+                    __syncwarp();
+                    __nv_bfloat16* dst =
+                        static_cast<__nv_bfloat16*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 8 * tp;
+                    for (int t = tr; t < live; t += 8)
+                        *reinterpret_cast<uint4*>(dst + (size_t)t * H * D) =
+                            *reinterpret_cast<const uint4*>(sOut + stage_at(t, tp));
+                } else {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_4d(&args.out[blockIdx.y], sOut, ch0, h, row0 + c * C, row_b);
+                        tc::bulk_commit();
+                    }
                 }
-                __syncwarp();
             }
             if (dots) {
                 arrive_warp(&b.dot_full);
@@ -663,24 +699,29 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 }
             }
         }
+        if (lane == 0) tc::bulk_wait_all();
     } else if (warp == S::EXTRA) {
-        // ------------------------------------------------------------------------ TMA, one lane
+        // ----------------------------------------------------- TMA (one lane), and the decays
         const CUtensorMap* map = args.map[blockIdx.y];
         const int hx = h / R.xg, hy = h / R.yg, hz = h / R.zg;
         const int row = a.sp.cu ? 0 : u.seq;
         const int tok0 = a.sp.cu ? (int)u.tok : u.index * a.sp.L;
+        const float u_scale = R.u_scale;
+        // (the raw decays are requested a chunk ahead: nothing waits for them)
+        auto raw = [&](int i) {
+            const long long tok = u.tok + (long long)chunk_at(i) * C + 2 * lane;
+            const int live = live_of(i) - 2 * lane;
+            float2 v = make_float2(0.f, 0.f);
+            if (live > 0) v.x = a.per_token ? __ldg(a.g + (size_t)tok * H + h) : __ldg(a.g + h);
+            if (live > 1) v.y = a.per_token ? __ldg(a.g + (size_t)(tok + 1) * H + h) : v.x;
+            return v;
+        };
+        float2 cur = raw(0), next = make_float2(0.f, 0.f);
         int sent = 0;
-        if (lane == 0) {
-            for (int i = 0; i < n; ++i) {
-                const int st = i % NS;
-                if (i >= NS) {            // (one lane: no vote)
-                    const unsigned long long t0 = now_ns();
-                    bool ok = true;
-                    while (!poll(&b.empty[st], (i / NS - 1) & 1)) {
-                        if (b.abort || now_ns() - t0 > kWaitNs) { b.abort = 1; ok = false; break; }
-                    }
-                    if (!ok) break;
-                }
+        for (int i = 0; i < n; ++i, cur = next) {
+            const int st = i % NS, gs = i % kGateRing, live = live_of(i);
+            if (i >= NS && !wait(b, &b.empty[st], (i / NS - 1) & 1)) break;
+            if (lane == 0) {
                 uint8_t* dst = sm + st * S::STAGE;
                 const int t = tok0 + chunk_at(i) * C;
                 tc::mbar_arrive_expect_tx(&b.full[st], S::STAGE);
@@ -692,132 +733,11 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                         tc::tma_load_4d(dst + 2 * kTile + k * kBlock, &map[0], 64 * k, hx, t, row,
                                         &b.full[st]);
                 }
-                sent = i + 1;
             }
-            // every copy has landed before the CTA leaves
-            for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) {
-                const unsigned long long t0 = now_ns();
-                while (!poll(&b.full[i % NS], (i / NS) & 1) && now_ns() - t0 < kWaitNs) {}
-            }
-        }
-        __syncwarp();
-    } else if (warp == S::EXTRA + 1) {
-        // -------------------------------------------------------------------------- tcgen05.mma
-        constexpr uint32_t id_sc = tc::idesc_bf16_f32(64, 64, 0, 0);
-        constexpr uint32_t id_o1 = tc::idesc_bf16_f32(128, 64, 0, 0);
-        constexpr uint32_t id_o2 = tc::idesc_bf16_f32(128, 64, 1, 0);
-        constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 128, 0, 1);
-        auto stage = [&](int i) { return tc::smem_u32(sm + (i % NS) * S::STAGE); };
-        auto scores = [&](int i) {
-            if (!wait(b, &b.full[i % NS], (i / NS) & 1)) return false;
-            if (a.sp.cu && live_of(i) < C) {
-                // packed: rows behind the sequence's end belong to the next one; they must not
-                // reach a product even as 0 x NaN
-                uint8_t* s = sm + (i % NS) * S::STAGE;
-                const int live = live_of(i), words = (C - live) * 8;     // 16-byte words per block
-                for (int k = 0; k < 2 * (S::STAGE / kTile); ++k)
-                    for (int w = lane; w < words; w += 32)
-                        *reinterpret_cast<uint4*>(s + k * kBlock + live * 128 + w * 16) =
-                            make_uint4(0, 0, 0, 0);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-            }
-            if constexpr (!kSummary) {
-                if (i > 0 && !wait(b, &b.sc_empty, (i - 1) & 1)) return false;
-                tc::tc_fence_after();
-                const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
-                const uint64_t yd = tc::smem_desc_sw128(stage(i), 16, 1024);
-#pragma unroll 1
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
-                    tc::mma_bf16_warp(tmem + kColSc, tc::desc_add(xd, off), tc::desc_add(yd, off),
-                                      id_sc, ks > 0);
-                }
-                tc::mma_commit_warp(&b.sc_full);
-            }
-            return true;
-        };
-        bool ok = scores(0);
-        int term = 0;
-        for (int i = 0; i < n && ok; ++i) {
-            // U: one term of the weighted Z after the other
-            if (i > 0 && !(ok = wait(b, &b.u_empty, (i - 1) & 1))) break;
-            const uint64_t yd = tc::smem_desc_sw128(stage(i), kBlock, 1024);
-            for (int k = 0; k < 3 && ok; ++k, ++term) {
-                const int slot = term % kWzRing;
-                if (!(ok = wait(b, &b.wz_full[slot], (term / kWzRing) & 1))) break;
-                tc::tc_fence_after();
-#pragma unroll 1
-                for (int ks = 0; ks < 4; ++ks)
-                    tc::mma_bf16_tmem_a_warp(tmem + kColU, tmem + kColWz + 32 * slot + 8 * ks,
-                                             tc::desc_add(yd, ks * 2048), id_u, (k > 0 || ks > 0));
-                tc::mma_commit_warp(&b.wz_empty[slot]);
-            }
-            if (!ok) break;
-            tc::mma_commit_warp(&b.u_full);
-            if constexpr (kSummary) {
-                tc::mma_commit_warp(&b.empty[i % NS]);
-                if (i + 1 < n) ok = scores(i + 1);
-                continue;
-            }
-            if (i + 1 < n && !(ok = scores(i + 1))) break;
-            // O1: the entering state read by X
-            if (!(ok = wait(b, &b.s_full, i & 1))) break;
-            if (i > 0 && !(ok = wait(b, &b.o_empty, (i - 1) & 1))) break;
-            tc::tc_fence_after();
-            const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
-#pragma unroll 1
-            for (int ks = 0; ks < 8; ++ks)
-                tc::mma_bf16_tmem_a_warp(tmem + kColO1, tmem + kColS + 8 * ks,
-                                         tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1,
-                                         ks > 0);
-            if constexpr (NP > 1) {
-#pragma unroll 1
-                for (int q = 0; q < NP - 1; ++q) {
-                    const uint64_t sd = tc::smem_desc_sw128(tc::smem_u32(sSlo) + q * D * D * 2, 16, 1024);
-#pragma unroll 1
-                    for (int ks = 0; ks < 8; ++ks)
-                        tc::mma_bf16_warp(tmem + kColO1,
-                                          tc::desc_add(sd, (ks >> 2) * (D * 128) + (ks & 3) * 32),
-                                          tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, 1);
-                }
-            }
-            tc::mma_commit_warp(&b.s_empty);
-            // O2: the chunk's own scores
-            const int buf = i % S::PBUF;
-            if (!(ok = wait(b, &b.p_full[buf], (i / S::PBUF) & 1))) break;
-            tc::tc_fence_after();
-            const uint64_t zd = tc::smem_desc_sw128(stage(i) + kTile, kBlock, 1024);
-#pragma unroll 1
-            for (int q = 0; q < NP; ++q) {
-                const uint64_t pd = tc::smem_desc_sw128(tc::smem_u32(sP) + (buf * NP + q) * kBlock, 16, 1024);
-#pragma unroll 1
-                for (int ks = 0; ks < 4; ++ks)
-                    tc::mma_bf16_warp(tmem + kColO2, tc::desc_add(zd, ks * 2048),
-                                      tc::desc_add(pd, ks * 32), id_o2, (q > 0 || ks > 0));
-            }
-            tc::mma_commit_warp(&b.p_empty[buf]);
-            tc::mma_commit_warp(&b.o_full);
-            tc::mma_commit_warp(&b.empty[i % NS]);
-        }
-        // every product has finished before the memory is given back
-        tc::mma_commit_warp(&b.drain);
-        const unsigned long long t0 = now_ns();
-        while (!poll(&b.drain, 0) && now_ns() - t0 < kWaitNs) {}
-        __syncwarp();
-    } else {
-        // ----------------------------------------------------------------------------- decays
-        auto pair = [&](int i, double* g0, double* g1) {
-            const long long tok = u.tok + (long long)chunk_at(i) * C;
-            const int live = live_of(i);
-            *g0 = log2_decay(a.g, a.per_token, tok + 2 * lane, H, h, 2 * lane < live);
-            *g1 = log2_decay(a.g, a.per_token, tok + 2 * lane + 1, H, h, 2 * lane + 1 < live);
-        };
-        double g0, g1, n0 = 0.0, n1 = 0.0;
-        pair(0, &g0, &g1);
-        for (int i = 0; i < n; ++i) {
-            const int gs = i % kGateRing, live = live_of(i);
-            if (i + 1 < n) pair(i + 1, &n0, &n1);
+            __syncwarp();
+            sent = i + 1;
+            if (i + 1 < n) next = raw(i + 1);
+            const double g0 = log2_decay(cur.x), g1 = log2_decay(cur.y);
             double s = g0 + g1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -835,16 +755,151 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 g.hi[t] = hi;
                 g.lo[t] = (float)(G[e] - (double)hi);
                 g.out[t] = rev ? up : down;
-                g.upd[t] = t < live ? (rev ? down : up) * R.u_scale : 0.f;
+                g.upd[t] = t < live ? (rev ? down : up) * u_scale : 0.f;
             }
             if (lane == 0) {
                 g.total = exp2f((float)all);
                 g.sum = all;
             }
             arrive_warp(&b.gfull[gs]);
-            g0 = n0;
-            g1 = n1;
         }
+        // every copy has landed before the CTA leaves
+        for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) {
+            const unsigned long long t0 = now_ns();
+            while (!poll(&b.full[i % NS], (i / NS) & 1) && now_ns() - t0 < kWaitNs) {}
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------- tcgen05.mma: U (+ 1), Sc (+ 2), O (+ 3)
+        const int role = warp - S::EXTRA - 1;
+        auto stage = [&](int i) { return tc::smem_u32(sm + (i % NS) * S::STAGE); };
+        // a chunk's tiles are in place; packed: rows behind the sequence's end belong to the next
+        // one and must not reach a product even as 0 x NaN, so the first role clears them
+        auto tiles = [&](int i) {
+            if (!wait(b, &b.full[i % NS], (i / NS) & 1)) return false;
+            if (a.sp.cu && live_of(i) < C) {
+                if (role == 0) {
+                    uint8_t* s = sm + (i % NS) * S::STAGE;
+                    const int live = live_of(i), words = (C - live) * 8;   // 16-byte words per block
+                    for (int k = 0; k < 2 * (S::STAGE / kTile); ++k)
+                        for (int w = lane; w < words; w += 32)
+                            *reinterpret_cast<uint4*>(s + k * kBlock + live * 128 + w * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    tc::fence_proxy_async_smem();
+                    arrive_warp(&b.tail);           // (one such chunk in a unit)
+                } else {
+                    if (!wait(b, &b.tail, 0)) return false;
+                    tc::fence_proxy_async_smem();
+                }
+            }
+            return true;
+        };
+        bool ok = true;
+        if (role == 0) {
+            constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 128, 0, 1);
+            int term = 0;
+            for (int i = 0; i < n && ok; ++i) {
+                if (!(ok = tiles(i))) break;
+                if (i > 0 && !(ok = wait(b, &b.u_empty, (i - 1) & 1))) break;
+                const uint64_t yd = tc::smem_desc_sw128(stage(i), kBlock, 1024);
+#pragma unroll 1
+                for (int k = 0; k < 3; ++k, ++term) {   // one term of the weighted Z after the other
+                    const int slot = term % kWzRing;
+                    if (!(ok = wait(b, &b.wz_full[slot], (term / kWzRing) & 1))) break;
+                    tc::tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_tmem_a(tmem + kColU, tmem + kColWz + 32 * slot + 8 * ks,
+                                       tc::desc_add(yd, ks * 2048), id_u, k + ks > 0);
+                        tc::mma_commit(&b.wz_empty[slot]);
+                        if (k == 2) {
+                            tc::mma_commit(&b.u_full);
+                            tc::mma_commit(&b.empty[i % NS]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (role == 1) {
+            constexpr uint32_t id_sc = tc::idesc_bf16_f32(64, 64, 0, 0);
+            for (int i = 0; i < n; ++i) {
+                if (!(ok = tiles(i))) break;
+                if (i > 0 && !(ok = wait(b, &b.sc_empty, (i - 1) & 1))) break;
+                tc::tc_fence_after();
+                const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
+                const uint64_t yd = tc::smem_desc_sw128(stage(i), 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
+                        tc::mma_bf16(tmem + kColSc, tc::desc_add(xd, off), tc::desc_add(yd, off), id_sc,
+                                     ks > 0);
+                    }
+                    tc::mma_commit(&b.sc_full);
+                    tc::mma_commit(&b.empty[i % NS]);
+                }
+                __syncwarp();
+            }
+        } else {
+            constexpr uint32_t id_o1 = tc::idesc_bf16_f32(128, 64, 0, 0);
+            constexpr uint32_t id_o2 = tc::idesc_bf16_f32(128, 64, 1, 0);
+            for (int i = 0; i < n; ++i) {
+                if (!(ok = tiles(i))) break;
+                if (i > 0 && !(ok = wait(b, &b.o_empty, (i - 1) & 1))) break;
+                // O1: the entering state read by X
+                if (!(ok = wait(b, &b.s_full, i & 1))) break;
+                tc::tc_fence_after();
+                const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_tmem_a(tmem + kColO1, tmem + kColS + 8 * ks,
+                                   tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, ks > 0);
+                    if constexpr (NP > 1) {
+#pragma unroll 1
+                        for (int q = 0; q < NP - 1; ++q) {
+                            const uint64_t sd =
+                                tc::smem_desc_sw128(tc::smem_u32(sSlo) + q * D * D * 2, 16, 1024);
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                tc::mma_bf16(tmem + kColO1,
+                                             tc::desc_add(sd, (ks >> 2) * (D * 128) + (ks & 3) * 32),
+                                             tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, 1);
+                        }
+                    }
+                    tc::mma_commit(&b.s_empty);
+                }
+                __syncwarp();
+                // O2: the chunk's own scores
+                const int buf = i % S::PBUF;
+                if (!(ok = wait(b, &b.p_full[buf], (i / S::PBUF) & 1))) break;
+                tc::tc_fence_after();
+                const uint64_t zd = tc::smem_desc_sw128(stage(i) + kTile, kBlock, 1024);
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int q = 0; q < NP; ++q) {
+                        const uint64_t pd =
+                            tc::smem_desc_sw128(tc::smem_u32(sP) + (buf * NP + q) * kBlock, 16, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_bf16(tmem + kColO2, tc::desc_add(zd, ks * 2048),
+                                         tc::desc_add(pd, ks * 32), id_o2, q + ks > 0);
+                    }
+                    tc::mma_commit(&b.p_empty[buf]);
+                    tc::mma_commit(&b.o_full);
+                    tc::mma_commit(&b.empty[i % NS]);
+                }
+                __syncwarp();
+            }
+        }
+        // every product has finished before the memory is given back
+        uint64_t* drain = &b.drain[role];
+        if (elect_one()) tc::mma_commit(drain);
+        __syncwarp();
+        const unsigned long long t0 = now_ns();
+        while (!poll(drain, 0) && now_ns() - t0 < kWaitNs) {}
+        __syncwarp();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -867,17 +922,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // [rows][T][heads][128] bf16 as {channel, head, token, row}; boxes of 64 channels x 64 tokens of
-// one head.  Tokens behind T read as zeros.
-bool encode(CUtensorMap* m, const void* base, int heads, int T, int rows) {
+// one head.  Tokens behind T read as zeros.  Stores: 32 channels, tokens behind T are not written.
+bool encode(CUtensorMap* m, const void* base, int heads, int T, int rows, bool store = false) {
     auto enc = encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)rows};
     const cuuint64_t row = D * 2;
     const cuuint64_t strides[3] = {row, row * heads, row * heads * T};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)C, 1};
+    const cuuint32_t box[4] = {store ? 32u : 64u, 1, (cuuint32_t)C, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -892,6 +947,8 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
         if ((!kSummary && !encode(&t.map[r][0], u.x, H / u.xg, a.sp.T, rows)) ||
             !encode(&t.map[r][1], u.y, H / u.yg, a.sp.T, rows) ||
             !encode(&t.map[r][2], u.z, H / u.zg, a.sp.T, rows))
+            return cudaErrorInvalidValue;
+        if (!kSummary && !u.out_f32 && !encode(&t.out[r], u.out, H, a.sp.T, rows, true))
             return cudaErrorInvalidValue;
     }
     auto kern = la_tc_kernel<NP, kSummary>;
