@@ -13,11 +13,12 @@
 // terms (24 bits, a ring of four 32-column slots), so that states are fp32-grade.  With NP = 3 the
 // scores and the state enter in three terms too (the state's second and third from shared memory).
 //
-// Roles (one CTA per SM, all of TMEM): warps 0-3 weight Z; 4-11 carry the state; 12-15 turn
-// scores into P and write the outputs; then one warp each for TMA and the decays, the products U,
-// the products Sc, and O1 with O2 (a poll of a barrier takes 80 cycles even when it is complete, so one
-// warp that issued all of them would be the slowest part).  They meet on mbarriers only, so a chunk's products overlap the neighbours' element work:
-// per chunk the tensor pipe needs 256 (Sc) + 768 (U) + 256 (O1) + 128 (O2) cycles at NP = 1.
+// Roles (one CTA per SM, all of TMEM): warps 0-7 weight Z; 8-15 carry the state and write the
+// outputs; 16-19 turn scores into P; then one warp each for the decays, the products U, Sc (and
+// TMA), and O1 with O2 (a poll of a barrier takes 80 cycles even when it is complete, so one warp
+// that issued all of them would be the slowest part).  They meet on mbarriers only, so a chunk's
+// products overlap the neighbours' element work: per chunk the tensor pipe needs 256 (Sc) + 768 (U)
+// + 256 (O1) + 200 (O2) cycles at NP = 1.
 // Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
 // once its copies and products have landed.
 #include <cuda.h>
@@ -35,7 +36,7 @@ constexpr int D = 128;                    // contracted and output channels
 constexpr int kTile = C * D * 2;          // bytes of one operand tile
 constexpr int kBlock = C * 128;           // 64 channels of it
 constexpr int kGateRing = 4, kWzRing = 4;
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kPolls = 1 << 18;
 
 // TMEM columns
 constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320, kColWz = 384;
@@ -50,8 +51,17 @@ struct TcArgs {
 
 struct GateSlot {
     float hi[C], lo[C], out[C], upd[C];
-    float total, pad[3];
-    double sum, pad2;
+    float total, pad[7];
+};
+
+// Position in a ring of N slots: the slot, and the parity of the phase that its n-th use completes.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) { slot = 0; phase ^= 1; }
+    }
 };
 
 template <int NP, bool kSummary>
@@ -66,8 +76,8 @@ struct TcShape {
     static constexpr int DOT = GATES + kGateRing * (int)sizeof(GateSlot);
     static constexpr int BARS = DOT + (kSummary ? 0 : 4 * C * 4);
     static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
-    static constexpr int EXTRA = kSummary ? 12 : 16;                     // first of the single warps
-    static constexpr int THREADS = (EXTRA + (kSummary ? 2 : 4)) * 32;    // (20 warps: 96 registers each)
+    static constexpr int EXTRA = kSummary ? 16 : 20;                     // first of the single warps
+    static constexpr int THREADS = (EXTRA + (kSummary ? 2 : 4)) * 32;
 };
 
 struct Bars {
@@ -80,35 +90,21 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-// One poll that lets the warp sleep until the phase completes, or for about 20 us: polls without
-// a time hint return early, and the issue slots that waiting warps then take slow the working ones.
-__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity) {
+// Bounded wait of a converged warp: false when it has run out (a poll sleeps for up to about 4 us,
+// so between 20 ms and a second).  Short and in line: the roles' hot code together has to stay in
+// the instruction cache (at 50 KB the element warps spent most of their time on instruction
+// fetches), and calls do not go with the warpgroups' register shares.
+__device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
-    return ok != 0;
-}
-// Whole-warp bounded wait; false once any wait of the CTA has run out.  The loop is kept out of
-// line: the roles' code together has to stay in the instruction cache.
-__device__ __noinline__ bool wait_on(Bars* b, uint64_t* bar, uint32_t parity) {
-    bool ok = true;
-    const unsigned long long t0 = now_ns();
-    while (!poll(bar, parity)) {
-        if (b->abort) { ok = false; break; }
-        if (now_ns() - t0 > kWaitNs) { b->abort = 1; ok = false; break; }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity)) || wait_on(&b, bar, parity);
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
+        "POLL:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra POLL;\n"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "n"(kPolls) : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    b.abort = 1;
+    return false;
 }
 __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
     __syncwarp();
@@ -126,6 +122,15 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low 
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Registers per thread of this warpgroup (all four warps).  A run launches with 80 (24 warps); the
+// shares below add up to 6 x 80, so every raise finds what the others gave back.
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+constexpr int kRegsZ = 64, kRegsState = 120, kRegsP = 64, kRegsSingle = 48;
+static_assert(2 * kRegsZ + 2 * kRegsState + kRegsP + kRegsSingle == 6 * 80, "register shares");
 
 // One lane of a converged warp.  A group of products issued by it in one unrolled run keeps the
 // tensor pipe fed (34 cycles per 128 x 64 x 16, 66 per 128 x 128 x 16); a loop of single products
@@ -231,13 +236,15 @@ __device__ __forceinline__ void stsm4t(uint32_t a, const uint32_t r[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
                  :: "r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
-// The output warps' staging: 64 tokens x 32 channels of bf16 per warp, 16-byte pieces swizzled so
+// The output warps' staging: 32 tokens x 32 channels of bf16 per warp, 16-byte pieces swizzled so
 // that eight neighbouring tokens lie in different banks.
 __device__ __forceinline__ uint32_t stage_at(uint32_t tok, uint32_t piece) {
     return tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4);
 }
 
-template <int NP, bool kSummary>
+// kF32: the outputs are fp32 (gradients that are still to be summed over a group of heads).  NP = 3
+// goes with products of the output rows (the decay gradient's need for precision is why it exists).
+template <int NP, bool kSummary, bool kF32>
 __global__ void __launch_bounds__(TcShape<NP, kSummary>::THREADS, 1)
 la_tc_kernel(const __grid_constant__ TcArgs args) {
     using S = TcShape<NP, kSummary>;
@@ -269,14 +276,14 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             tc::mbar_init(&b.full[i], 1);
-            tc::mbar_init(&b.empty[i], kSummary ? 5 : 7);   // the products; four warps that read Z
+            tc::mbar_init(&b.empty[i], kSummary ? 9 : 11);  // the products; eight warps that read Z
         }
         for (int i = 0; i < kGateRing; ++i) {
             tc::mbar_init(&b.gfull[i], 1);
             tc::mbar_init(&b.gempty[i], S::EXTRA);    // every element warp
         }
         for (int i = 0; i < kWzRing; ++i) {
-            tc::mbar_init(&b.wz_full[i], 4);
+            tc::mbar_init(&b.wz_full[i], 8);
             tc::mbar_init(&b.wz_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -290,8 +297,8 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         tc::mbar_init(&b.s_full, 8);
         tc::mbar_init(&b.s_empty, 1);
         tc::mbar_init(&b.o_full, 1);
-        tc::mbar_init(&b.o_empty, 4);
-        tc::mbar_init(&b.dot_full, 4);
+        tc::mbar_init(&b.o_empty, 8);
+        tc::mbar_init(&b.dot_full, 8);
         tc::mbar_init(&b.dot_empty, 1);
         tc::mbar_init(&b.fin_full, 8);
         tc::mbar_init(&b.tail, 1);
@@ -303,71 +310,65 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = b.tmem;
+    if constexpr (!kSummary) {        // (one instruction per warpgroup)
+        if (warp < 8) regs_down<kRegsZ>();
+        else if (warp < 16) regs_up<kRegsState>();
+        else if (warp < 20) regs_down<kRegsP>();
+        else regs_down<kRegsSingle>();
+    }
 
-    if (warp < 4) {
-        // ---------------------------------- weighted Z: 32 output channels a warp, 16 at a time.
+    if (warp < 8) {
+        // --------------------------------------------- weighted Z: 16 output channels a warp.
         // ldmatrix leaves the transposed tile in the layout that the 16-lane TMEM store takes.
-        const int m = lane >> 3;
-        const uint32_t zrow = ((m >> 1) * 8 + (lane & 7)) * 128 + (quarter >> 1) * kBlock;
-        const uint32_t zch = (quarter & 1) * 4 + (m & 1);        // 16-byte piece of the first half
-        int term = 0;
+        const int m = lane >> 3, e = warp >> 2;
+        const uint32_t zat = ((m >> 1) * 8 + (lane & 7)) * 128 + (quarter >> 1) * kBlock +
+                             ((((quarter & 1) * 4 + 2 * e + (m & 1)) ^ (lane & 7)) << 4);
+        const uint32_t to = tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColWz);
+        const bool packed = a.sp.cu != nullptr;
+        Ring<NS> at;
+        Ring<kGateRing> gp;
+        Ring<kWzRing> wz;
+        const uint32_t z0 = tc::smem_u32(sm) + kTile + zat;
+#pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            const int st = i % NS, gs = i % kGateRing;
-            if (!wait(b, &b.full[st], (i / NS) & 1) || !wait(b, &b.gfull[gs], (i / kGateRing) & 1))
-                break;
-            const uint32_t z = tc::smem_u32(sm + st * S::STAGE + kTile) + zrow;
-            uint32_t p[2][16];                  // [half][4 tb + m]: tokens 16 tb + 8 (m / 2) ..
+            if (!wait(b, &b.full[at.slot], at.phase) || !wait(b, &b.gfull[gp.slot], gp.phase)) break;
+            if (packed && live_of(i) < C && !wait(b, &b.tail, 0)) break;
+            const uint32_t z = z0 + at.slot * S::STAGE;
+            const float* upd = gates[gp.slot].upd + 2 * (lane & 3);
+            uint32_t p[16];                     // [4 tb + m]: tokens 16 tb + 8 (m / 2) ..
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb)
-                    ldsm4t(&p[e][4 * tb], z + tb * 2048 + (((zch + 2 * e) ^ (lane & 7)) << 4));
-            arrive_warp(&b.empty[st]);
-            const int live = live_of(i);
-            if (live < C) {                     // (rows behind the sequence's end are not its own)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int t = (j >> 2) * 16 + ((j >> 1) & 1) * 8 + 2 * (lane & 3);
-                    const uint32_t keep = t + 1 < live ? 0xffffffffu : t < live ? 0xffffu : 0u;
-                    p[0][j] &= keep;
-                    p[1][j] &= keep;
-                }
-            }
-            float2 v[2][16];
+            for (int tb = 0; tb < 4; ++tb) ldsm4t(&p[4 * tb], z + tb * 2048);
+            float2 v[16];
 #pragma unroll
             for (int g = 0; g < 8; ++g) {       // 8 tokens
-                const float2 w = *reinterpret_cast<const float2*>(gates[gs].upd + 8 * g + 2 * (lane & 3));
+                const float2 w = *reinterpret_cast<const float2*>(upd + 8 * g);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t x = p[e][2 * g + k];
-                        v[e][2 * g + k] = mul2(make_float2(lo_f(x), hi_f(x)), w);
-                    }
+                for (int k = 0; k < 2; ++k)
+                    v[2 * g + k] = mul2(make_float2(lo_f(p[2 * g + k]), hi_f(p[2 * g + k])), w);
             }
-            arrive_warp(&b.gempty[gs]);
+            arrive_warp(&b.empty[at.slot]);
+            arrive_warp(&b.gempty[gp.slot]);
+            at.next();
+            gp.next();
             bool ok = true;
 #pragma unroll 1
-            for (int k = 0; k < 3; ++k, ++term) {        // (one body: the third leaves zero)
-                const int slot = term % kWzRing;
-                if (term >= kWzRing && !(ok = wait(b, &b.wz_empty[slot], (term / kWzRing - 1) & 1))) break;
+            for (int k = 0; k < 3; ++k) {
+                if (3 * i + k >= kWzRing && !(ok = wait(b, &b.wz_empty[wz.slot], wz.phase ^ 1))) break;
                 tc::tc_fence_after();
+                uint32_t t[16];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t t[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) t[j] = cut2(v[e][j]);
-                    tmem_st_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColWz + 32 * slot), t);
-                }
+                for (int j = 0; j < 16; ++j) t[j] = cut2(v[j]);
+                tmem_st_16x32(to + 32 * wz.slot, t);
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
-                arrive_warp(&b.wz_full[slot]);
+                arrive_warp(&b.wz_full[wz.slot]);
+                wz.next();
             }
             if (!ok) break;
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------ the state: 64 contracted channels of one row
-        const int row = 32 * quarter + lane, half = (warp - 4) >> 2, col0 = 64 * half;
+        const int row = 32 * quarter + lane, half = (warp - 8) >> 2, col0 = 64 * half;
         const int rs = R.transposed ? D : 1, cs = R.transposed ? 1 : D;
         const size_t seq_state = ((size_t)u.seq * H + h) * (D * D);
         const size_t unit_state = ((size_t)unit * H + h) * (D * D);
@@ -382,47 +383,192 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int j = 0; j < 32; ++j)
             st[j] = init ? make_float2(init[own + (size_t)(2 * j) * cs], init[own + (size_t)(2 * j + 1) * cs])
                          : make_float2(0.f, 0.f);
-        double decay = 0.0;
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int gs = i % kGateRing;
-            if constexpr (!kSummary) {
-                if (i > 0 && !(ok = wait(b, &b.s_empty, (i - 1) & 1))) break;
-                tc::tc_fence_after();
+        auto put_state = [&](int i) {             // the state entering chunk i, as an operand
+            if (i > 0 && !wait(b, &b.s_empty, (i - 1) & 1)) return false;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t t[8];
+                if constexpr (NP == 1) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) t[j] = pack2(st[8 * k + j].x, st[8 * k + j].y);
+                } else {
+                    // three terms: the first through TMEM, the others through shared memory
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t m[4], l[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float2 x = st[8 * k + 4 * q + j];
+                            t[4 * q + j] = cut2(x);
+                            m[j] = cut2(x);
+                            l[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+                        }
+                        uint8_t* at = sSlo + half * (D * 128) + row * 128 + (((2 * k + q) ^ (row & 7)) << 4);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(m[0], m[1], m[2], m[3]);
+                        *reinterpret_cast<uint4*>(at + D * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
+                }
+                tmem_st8(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half + 8 * k), t);
+            }
+            tc::tmem_st_wait();
+            if constexpr (NP > 1) tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            arrive_warp(&b.s_full);
+            return true;
+        };
+        // Outputs: this warp's 32 channels, 32 of the chunk's tokens
+        const int gr = lane >> 2, gc = 2 * (lane & 3);
+        const int ch0 = 32 * quarter, tq = 32 * half;
+        const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
+        const int m4 = lane >> 3;                                // matrix of an x4 access
+        uint8_t* sOut = sSlo + S::SLO + (warp - 8) * (kTile / 8);
+        constexpr bool dots = !kSummary && NP > 1;
+        const float o_scale = R.o_scale;
+        auto put_out = [&](int i) {
+            const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i) - tq;
+            const long long tok = u.tok + (long long)c * C + tq;
+            if (lane == 0) tc::bulk_wait_read_all();             // the staging area is free again
+            __syncwarp();
+            if constexpr (dots) {
+                // the rows that the outputs are multiplied with, into the staging area
+                const int Hd = H / R.dg;
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.dot) +
+                                           ((size_t)tok * Hd + h / R.dg) * D + ch0 + 8 * tp;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t t[8];
-                    if constexpr (NP == 1) {
+                    const int t = 8 * k + tr;
+                    uint4 w = make_uint4(0, 0, 0, 0);
+                    if (t < live) w = __ldg(reinterpret_cast<const uint4*>(src + (size_t)t * Hd * D));
+                    *reinterpret_cast<uint4*>(sOut + stage_at(t, tp)) = w;
+                }
+                __syncwarp();
+            }
+            if (!wait(b, &b.o_full, i & 1)) return false;
+            tc::tc_fence_after();
+            float2 dot[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) t[j] = pack2(st[8 * k + j].x, st[8 * k + j].y);
-                    } else {
-                        // three terms: the first through TMEM, the others through shared memory
+            for (int j = 0; j < 4; ++j) dot[j] = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {                        // 16 channels
+                float2 x[8], y[8];
+                tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO1 + tq), x);
+                tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO2 + tq), y);
+                ld_wait(x, y);
+                if (e == 1) {
+                    tc::tc_fence_before();
+                    arrive_warp(&b.o_empty);
+                }
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            uint32_t m[4], l[4];
+                for (int j = 0; j < 4; ++j) {
+                    const float2 g = *reinterpret_cast<const float2*>(gates[gs].out + tq + 8 * j + gc);
+                    const float2 w = mul2(g, make_float2(o_scale, o_scale));
+                    x[2 * j] = fma2(x[2 * j], w, y[2 * j]);
+                    x[2 * j + 1] = fma2(x[2 * j + 1], w, y[2 * j + 1]);
+                }
+                if constexpr (dots) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float2 x = st[8 * k + 4 * q + j];
-                                t[4 * q + j] = cut2(x);
-                                m[j] = cut2(x);
-                                l[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
-                            }
-                            uint8_t* at = sSlo + half * (D * 128) + row * 128 + (((2 * k + q) ^ (row & 7)) << 4);
-                            *reinterpret_cast<uint4*>(at) = make_uint4(m[0], m[1], m[2], m[3]);
-                            *reinterpret_cast<uint4*>(at + D * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
+                    for (int j = 0; j < 2; ++j) {                // 16 tokens: four 8 x 8 matrices
+                        uint32_t d[4];
+                        ldsm4t(d, tc::smem_u32(sOut) +
+                                      stage_at(16 * j + 8 * (m4 >> 1) + (lane & 7), 2 * e + (m4 & 1)));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            dot[2 * j + (k >> 1)] = fma2(x[4 * j + k], make_float2(lo_f(d[k]), hi_f(d[k])),
+                                                         dot[2 * j + (k >> 1)]);
+                    }
+                    __syncwarp();
+                }
+                if constexpr (!kF32) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) o[k] = pack2(x[4 * j + k].x, x[4 * j + k].y);
+                        stsm4t(tc::smem_u32(sOut) +
+                                   stage_at(16 * j + 8 * (m4 >> 1) + (lane & 7), 2 * e + (m4 & 1)), o);
+                    }
+                } else {
+                    float* dst = static_cast<float*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 16 * e + gr;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int t = 8 * (j >> 1) + gc;
+                        float* at = dst + (size_t)t * H * D + 8 * (j & 1);
+                        if (t < live) at[0] = x[j].x;
+                        if (t + 1 < live) at[(size_t)H * D] = x[j].y;
+                    }
+                }
+            }
+            arrive_warp(&b.gempty[gs]);
+            if constexpr (!kF32) {
+                if (a.sp.cu && live < 32) {       // (the rows behind are another sequence's)
+                    __syncwarp();
+                    __nv_bfloat16* dst =
+                        static_cast<__nv_bfloat16*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 8 * tp;
+                    for (int t = tr; t < live; t += 8)
+                        *reinterpret_cast<uint4*>(dst + (size_t)t * H * D) =
+                            *reinterpret_cast<const uint4*>(sOut + stage_at(t, tp));
+                } else if (live > 0) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::tma_store_4d(&args.out[blockIdx.y], sOut, ch0, h,
+                                         (a.sp.cu ? (int)u.tok : u.index * a.sp.L) + c * C + tq,
+                                         a.sp.cu ? 0 : u.seq);
+                        tc::bulk_commit();
+                    }
+                }
+            }
+            if constexpr (dots) {
+                // sum over the lanes that hold other channels
+#pragma unroll
+                for (int s = 2; s > 0; s >>= 1)
+#pragma unroll
+                    for (int j = 0; j < s; ++j) {
+                        const bool up = lane & (8 * s);
+                        const float2 send = up ? dot[j] : dot[j + s], keep = up ? dot[j + s] : dot[j];
+                        dot[j].x = keep.x + __shfl_xor_sync(0xffffffffu, send.x, 8 * s);
+                        dot[j].y = keep.y + __shfl_xor_sync(0xffffffffu, send.y, 8 * s);
+                    }
+                dot[0].x += __shfl_xor_sync(0xffffffffu, dot[0].x, 4);
+                dot[0].y += __shfl_xor_sync(0xffffffffu, dot[0].y, 4);
+                if (i > 0 && !wait(b, &b.dot_empty, (i - 1) & 1)) return false;
+                if (!(lane & 4))
+                    *reinterpret_cast<float2*>(sDot + quarter * C + tq + 8 * (lane >> 3) + gc) = dot[0];
+                arrive_warp(&b.dot_full);
+                if (warp == 8) {
+                    if (!wait(b, &b.dot_full, i & 1)) return false;
+                    const int all = live_of(i);
+                    const long long t0 = u.tok + (long long)c * C;
+                    double sum = 0.0;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = 32 * e + lane;
+                        const float s = (sDot[t] + sDot[C + t]) + (sDot[2 * C + t] + sDot[3 * C + t]);
+                        if (t < all) {
+                            R.dot_out[(size_t)(t0 + t) * H + h] = s;
+                            sum += (double)s;
                         }
                     }
-                    tmem_st8(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half + 8 * k), t);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0)
+                        R.dot_sum[(size_t)la_chunk_id(u.tok - (long long)u.index * a.sp.L, u.seq,
+                                                      u.index * (a.sp.L / C) + c) * H + h] = sum;
+                    arrive_warp(&b.dot_empty);
                 }
-                tc::tmem_st_wait();
-                if constexpr (NP > 1) tc::fence_proxy_async_smem();
-                tc::tc_fence_before();
-                arrive_warp(&b.s_full);
             }
+            return true;
+        };
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int gs = i % kGateRing;
+            if constexpr (!kSummary)
+                if (!(ok = put_state(i))) break;
             if (!(ok = wait(b, &b.gfull[gs], (i / kGateRing) & 1))) break;
             const float2 total = make_float2(gates[gs].total, gates[gs].total);
-            if constexpr (kSummary) decay += gates[gs].sum;
-            arrive_warp(&b.gempty[gs]);
+            if constexpr (kSummary) arrive_warp(&b.gempty[gs]);
             if (!(ok = wait(b, &b.u_full, i & 1))) break;
             tc::tc_fence_after();
 #pragma unroll
@@ -435,7 +581,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
             tc::tc_fence_before();
             arrive_warp(&b.u_empty);
+            if constexpr (!kSummary)
+                if (!(ok = put_out(i))) break;
         }
+        if (!kSummary && lane == 0) tc::bulk_wait_all();
         if (ok) {
             float* fin = kSummary ? R.unit_state + unit_state
                                   : (!R.unit_state && R.fin ? R.fin + seq_state : nullptr);
@@ -446,7 +595,6 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                     fin[own + (size_t)(2 * j + 1) * cs] = st[j].y;
                 }
             }
-            if (kSummary && warp == 4 && lane == 0) R.unit_decay[(size_t)unit * H + h] = decay;
             if (!kSummary && !R.unit_state && R.fin_dot) {
                 const float* f = R.fin_dot + seq_state + own;
                 double d = 0.0;
@@ -456,21 +604,20 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                          (double)st[j].y * (double)f[(size_t)(2 * j + 1) * cs];
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                if (lane == 0) b.fin[warp - 4] = d;
+                if (lane == 0) b.fin[warp - 8] = d;
                 arrive_warp(&b.fin_full);
-                if (warp == 4 && wait(b, &b.fin_full, 0) && lane == 0) {
+                if (warp == 8 && wait(b, &b.fin_full, 0) && lane == 0) {
                     double s = 0.0;
                     for (int w = 0; w < 8; ++w) s += b.fin[w];
                     R.fin_dot_out[(size_t)u.seq * H + h] = s;
                 }
             }
         }
-    } else if (warp < S::EXTRA) {
-        // ------------------------------------------------------------ P from scores, and outputs
+    } else if (!kSummary && warp < S::EXTRA) {
+        // -------------------------------------------------------------------- P from the scores
         constexpr int PB = S::PBUF;
         const int gr = lane >> 2, gc = 2 * (lane & 3);
-        const float p_scale = R.p_scale, o_scale = R.o_scale;
-        uint8_t* sOut = sSlo + S::SLO + (warp - 12) * (kTile / 4);
+        const float p_scale = R.p_scale;
         // P is zero beyond the diagonal: those 16 x 8 tiles are cleared once and stay
         for (int k = 0; k < PB * NP; ++k)
             for (int w = lane; w < 16 * 8; w += 32) {
@@ -554,190 +701,34 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
             tc::tc_fence_before();
             arrive_warp(&b.sc_empty);
+            arrive_warp(&b.gempty[gs]);
             tc::fence_proxy_async_smem();
             arrive_warp(&b.p_full[buf]);
             return true;
         };
-        const int ch0 = 32 * quarter;                            // this warp's output channels
-        const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
-        const int m = lane >> 3;                                 // matrix of an x4 access
-        const bool dots = R.dot != nullptr, out_f32 = R.out_f32;
-        const int row_b = a.sp.cu ? 0 : u.seq, row0 = a.sp.cu ? (int)u.tok : u.index * a.sp.L;
-        bool ok = make_p(0);
-        for (int i = 0; i < n && ok; ++i) {
-            if (i + 1 < n && !(ok = make_p(i + 1))) break;
-            const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i);
-            const long long tok = u.tok + (long long)c * C;
-            if (lane == 0) tc::bulk_wait_read_all();             // the staging area is free again
-            __syncwarp();
-            if (dots) {
-                // the rows that the outputs are multiplied with, into the staging area
-                const int Hd = H / R.dg;
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.dot) +
-                                           ((size_t)tok * Hd + h / R.dg) * D + ch0 + 8 * tp;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int t = 8 * k + tr;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (t < live) w = __ldg(reinterpret_cast<const uint4*>(src + (size_t)t * Hd * D));
-                    *reinterpret_cast<uint4*>(sOut + stage_at(t, tp)) = w;
-                }
-                __syncwarp();
-            }
-            if (!(ok = wait(b, &b.o_full, i & 1))) break;
-            tc::tc_fence_after();
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {                        // 32 tokens
-                float2 w[4], dot[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[j] = *reinterpret_cast<const float2*>(gates[gs].out + 32 * q + 8 * j + gc);
-                    w[j].x *= o_scale;
-                    w[j].y *= o_scale;
-                    dot[j] = make_float2(0.f, 0.f);
-                }
-#pragma unroll 1
-                for (int e = 0; e < 2; ++e) {                    // 16 channels
-                    float2 x[8], y[8];
-                    tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO1 + 32 * q), x);
-                    tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO2 + 32 * q), y);
-                    ld_wait(x, y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = fma2(x[j], w[j >> 1], y[j]);
-                    if (dots) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {            // 16 tokens: four 8 x 8 matrices
-                            uint32_t d[4];
-                            ldsm4t(d, tc::smem_u32(sOut) +
-                                          stage_at(32 * q + 16 * j + 8 * (m >> 1) + (lane & 7), 2 * e + (m & 1)));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                dot[2 * j + (k >> 1)] = fma2(x[4 * j + k], make_float2(lo_f(d[k]), hi_f(d[k])),
-                                                             dot[2 * j + (k >> 1)]);
-                        }
-                        __syncwarp();
-                    }
-                    if (!out_f32) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) o[k] = pack2(x[4 * j + k].x, x[4 * j + k].y);
-                            stsm4t(tc::smem_u32(sOut) +
-                                       stage_at(32 * q + 16 * j + 8 * (m >> 1) + (lane & 7), 2 * e + (m & 1)), o);
-                        }
-                    } else {
-                        float* dst = static_cast<float*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 16 * e + gr;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int t = 32 * q + 8 * (j >> 1) + gc;
-                            float* at = dst + (size_t)t * H * D + 8 * (j & 1);
-                            if (t < live) at[0] = x[j].x;
-                            if (t + 1 < live) at[(size_t)H * D] = x[j].y;
-                        }
-                    }
-                }
-                if (dots) {
-                    if (q == 0 && i > 0 && !(ok = wait(b, &b.dot_empty, (i - 1) & 1))) break;
-                    // sum over the lanes that hold other channels
-#pragma unroll
-                    for (int s = 2; s > 0; s >>= 1)
-#pragma unroll
-                        for (int j = 0; j < s; ++j) {
-                            const bool up = lane & (8 * s);
-                            const float2 send = up ? dot[j] : dot[j + s], keep = up ? dot[j + s] : dot[j];
-                            dot[j].x = keep.x + __shfl_xor_sync(0xffffffffu, send.x, 8 * s);
-                            dot[j].y = keep.y + __shfl_xor_sync(0xffffffffu, send.y, 8 * s);
-                        }
-                    dot[0].x += __shfl_xor_sync(0xffffffffu, dot[0].x, 4);
-                    dot[0].y += __shfl_xor_sync(0xffffffffu, dot[0].y, 4);
-                    if (!(lane & 4))
-                        *reinterpret_cast<float2*>(sDot + quarter * C + 32 * q + 8 * (lane >> 3) + gc) = dot[0];
-                }
-            }
-            if (!ok) break;
-            tc::tc_fence_before();
-            arrive_warp(&b.o_empty);
-            arrive_warp(&b.gempty[gs]);
-            if (!out_f32) {
-                if (a.sp.cu && live < C) {        // (the rows behind are another sequence's)
-                    __syncwarp();
-                    __nv_bfloat16* dst =
-                        static_cast<__nv_bfloat16*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 8 * tp;
-                    for (int t = tr; t < live; t += 8)
-                        *reinterpret_cast<uint4*>(dst + (size_t)t * H * D) =
-                            *reinterpret_cast<const uint4*>(sOut + stage_at(t, tp));
-                } else {
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::tma_store_4d(&args.out[blockIdx.y], sOut, ch0, h, row0 + c * C, row_b);
-                        tc::bulk_commit();
-                    }
-                }
-            }
-            if (dots) {
-                arrive_warp(&b.dot_full);
-                if (quarter == 0) {
-                    if (!(ok = wait(b, &b.dot_full, i & 1))) break;
-                    double sum = 0.0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = 32 * e + lane;
-                        const float s = (sDot[t] + sDot[C + t]) + (sDot[2 * C + t] + sDot[3 * C + t]);
-                        if (t < live) {
-                            R.dot_out[(size_t)(tok + t) * H + h] = s;
-                            sum += (double)s;
-                        }
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0)
-                        R.dot_sum[(size_t)la_chunk_id(u.tok - (long long)u.index * a.sp.L, u.seq,
-                                                      u.index * (a.sp.L / C) + c) * H + h] = sum;
-                    arrive_warp(&b.dot_empty);
-                }
-            }
-        }
-        if (lane == 0) tc::bulk_wait_all();
+        for (int i = 0; i < n; ++i)
+            if (!make_p(i)) break;
     } else if (warp == S::EXTRA) {
-        // ----------------------------------------------------- TMA (one lane), and the decays
-        const CUtensorMap* map = args.map[blockIdx.y];
-        const int hx = h / R.xg, hy = h / R.yg, hz = h / R.zg;
-        const int row = a.sp.cu ? 0 : u.seq;
-        const int tok0 = a.sp.cu ? (int)u.tok : u.index * a.sp.L;
+        // -------------------------------------------------------------------------- the decays
         const float u_scale = R.u_scale;
-        // (the raw decays are requested a chunk ahead: nothing waits for them)
-        auto raw = [&](int i) {
-            const long long tok = u.tok + (long long)chunk_at(i) * C + 2 * lane;
-            const int live = live_of(i) - 2 * lane;
-            float2 v = make_float2(0.f, 0.f);
-            if (live > 0) v.x = a.per_token ? __ldg(a.g + (size_t)tok * H + h) : __ldg(a.g + h);
-            if (live > 1) v.y = a.per_token ? __ldg(a.g + (size_t)(tok + 1) * H + h) : v.x;
-            return v;
+        // The raw decays are requested a chunk ahead (and stay requested there: volatile), clamped to
+        // the unit and unconditional, so that nothing depends on them before they are used.
+        const float* gp = a.g + h + (a.per_token ? (size_t)u.tok * H : 0);
+        const size_t gstep = a.per_token ? H : 0;
+        auto load = [&](int t) {
+            float x;
+            asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(gp + min(t, u.len - 1) * gstep));
+            return x;
         };
-        float2 cur = raw(0), next = make_float2(0.f, 0.f);
-        int sent = 0;
+        int t0 = chunk_at(0) * C + 2 * lane;
+        float2 cur = make_float2(load(t0), load(t0 + 1)), next;
+        double decay = 0.0;
         for (int i = 0; i < n; ++i, cur = next) {
-            const int st = i % NS, gs = i % kGateRing, live = live_of(i);
-            if (i >= NS && !wait(b, &b.empty[st], (i / NS - 1) & 1)) break;
-            if (lane == 0) {
-                uint8_t* dst = sm + st * S::STAGE;
-                const int t = tok0 + chunk_at(i) * C;
-                tc::mbar_arrive_expect_tx(&b.full[st], S::STAGE);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    tc::tma_load_4d(dst + k * kBlock, &map[1], 64 * k, hy, t, row, &b.full[st]);
-                    tc::tma_load_4d(dst + kTile + k * kBlock, &map[2], 64 * k, hz, t, row, &b.full[st]);
-                    if constexpr (!kSummary)
-                        tc::tma_load_4d(dst + 2 * kTile + k * kBlock, &map[0], 64 * k, hx, t, row,
-                                        &b.full[st]);
-                }
-            }
-            __syncwarp();
-            sent = i + 1;
-            if (i + 1 < n) next = raw(i + 1);
-            const double g0 = log2_decay(cur.x), g1 = log2_decay(cur.y);
+            const int gs = i % kGateRing, live = live_of(i);
+            t0 = chunk_at(min(i + 1, n - 1)) * C + 2 * lane;
+            next = make_float2(load(t0), load(t0 + 1));
+            const double g0 = 2 * lane < live ? log2_decay(cur.x) : 0.0;
+            const double g1 = 2 * lane + 1 < live ? log2_decay(cur.y) : 0.0;
             double s = g0 + g1;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -745,43 +736,45 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 if (lane >= o) s += x;
             }
             const double all = __shfl_sync(0xffffffffu, s, 31);
+            if constexpr (kSummary) decay += all;
             const double G[2] = {s - g1, s};
             if (i >= kGateRing && !wait(b, &b.gempty[gs], (i / kGateRing - 1) & 1)) break;
             GateSlot& g = gates[gs];
+            float up[2], down[2], hi[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const float hi = (float)G[e], down = exp2f(hi), up = exp2f((float)(all - G[e]));
-                g.hi[t] = hi;
-                g.lo[t] = (float)(G[e] - (double)hi);
-                g.out[t] = rev ? up : down;
-                g.upd[t] = t < live ? (rev ? down : up) * u_scale : 0.f;
+                hi[e] = (float)G[e];
+                lo[e] = (float)(G[e] - (double)hi[e]);
+                down[e] = ex2(hi[e]);
+                up[e] = ex2((float)(all - G[e]));
             }
-            if (lane == 0) {
-                g.total = exp2f((float)all);
-                g.sum = all;
-            }
+            const int t = 2 * lane;
+            *reinterpret_cast<float2*>(g.hi + t) = make_float2(hi[0], hi[1]);
+            *reinterpret_cast<float2*>(g.lo + t) = make_float2(lo[0], lo[1]);
+            *reinterpret_cast<float2*>(g.out + t) = rev ? make_float2(up[0], up[1]) : make_float2(down[0], down[1]);
+            *reinterpret_cast<float2*>(g.upd + t) =
+                make_float2(t < live ? (rev ? down[0] : up[0]) * u_scale : 0.f,
+                            t + 1 < live ? (rev ? down[1] : up[1]) * u_scale : 0.f);
+            if (lane == 0) g.total = ex2((float)all);
             arrive_warp(&b.gfull[gs]);
         }
-        // every copy has landed before the CTA leaves
-        for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) {
-            const unsigned long long t0 = now_ns();
-            while (!poll(&b.full[i % NS], (i / NS) & 1) && now_ns() - t0 < kWaitNs) {}
-        }
-        __syncwarp();
+        if (kSummary && lane == 0) R.unit_decay[(size_t)unit * H + h] = decay;
     } else {
         // ---------------------------------------------- tcgen05.mma: U (+ 1), Sc (+ 2), O (+ 3)
         const int role = warp - S::EXTRA - 1;
-        auto stage = [&](int i) { return tc::smem_u32(sm + (i % NS) * S::STAGE); };
+        const bool packed = a.sp.cu != nullptr;
+        Ring<NS> at;                                      // of the chunk being worked on
         // a chunk's tiles are in place; packed: rows behind the sequence's end belong to the next
         // one and must not reach a product even as 0 x NaN, so the first role clears them
         auto tiles = [&](int i) {
-            if (!wait(b, &b.full[i % NS], (i / NS) & 1)) return false;
-            if (a.sp.cu && live_of(i) < C) {
+            if (!wait(b, &b.full[at.slot], at.phase)) return false;
+            if (packed && live_of(i) < C) {
                 if (role == 0) {
-                    uint8_t* s = sm + (i % NS) * S::STAGE;
+                    uint8_t* s = sm + at.slot * S::STAGE;
                     const int live = live_of(i), words = (C - live) * 8;   // 16-byte words per block
+#pragma unroll 1
                     for (int k = 0; k < 2 * (S::STAGE / kTile); ++k)
+#pragma unroll 1
                         for (int w = lane; w < words; w += 32)
                             *reinterpret_cast<uint4*>(s + k * kBlock + live * 128 + w * 16) =
                                 make_uint4(0, 0, 0, 0);
@@ -794,63 +787,103 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
             return true;
         };
+        // TMA: the role that needs a chunk first requests the one that takes a freed stage
+        const CUtensorMap* map = args.map[blockIdx.y];
+        const int hx = h / R.xg, hy = h / R.yg, hz = h / R.zg, brow = packed ? 0 : u.seq;
+        const int tok0 = packed ? (int)u.tok : u.index * a.sp.L;
+        Ring<NS> req;
+        int sent = 0;
+        auto request = [&](int i) {
+            if (i >= NS && !wait(b, &b.empty[req.slot], req.phase ^ 1)) return false;
+            if (elect_one()) {
+                uint64_t* full = &b.full[req.slot];
+                uint8_t* dst = sm + req.slot * S::STAGE;
+                const int t = tok0 + chunk_at(i) * C;
+                tc::mbar_arrive_expect_tx(full, S::STAGE);
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k, dst += kBlock) {
+                    tc::tma_load_4d(dst, &map[1], 64 * k, hy, t, brow, full);
+                    tc::tma_load_4d(dst + kTile, &map[2], 64 * k, hz, t, brow, full);
+                    if constexpr (!kSummary)
+                        tc::tma_load_4d(dst + 2 * kTile, &map[0], 64 * k, hx, t, brow, full);
+                }
+            }
+            __syncwarp();
+            req.next();
+            sent = i + 1;
+            return true;
+        };
         bool ok = true;
-        if (role == 0) {
+        if (kSummary || role == 0) {
             constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 128, 0, 1);
-            int term = 0;
-            for (int i = 0; i < n && ok; ++i) {
+            const uint64_t yd0 = tc::smem_desc_sw128(tc::smem_u32(sm), kBlock, 1024);
+            Ring<kWzRing> wz;
+#pragma unroll 1
+            for (int i = kSummary ? 1 - NS : 0; i < n && ok; ++i) {
+                if (kSummary && i + NS - 1 < n && !(ok = request(i + NS - 1))) break;
+                if (kSummary && i < 0) continue;
                 if (!(ok = tiles(i))) break;
                 if (i > 0 && !(ok = wait(b, &b.u_empty, (i - 1) & 1))) break;
-                const uint64_t yd = tc::smem_desc_sw128(stage(i), kBlock, 1024);
+                const uint64_t yd = tc::desc_add(yd0, at.slot * S::STAGE);
 #pragma unroll 1
-                for (int k = 0; k < 3; ++k, ++term) {   // one term of the weighted Z after the other
-                    const int slot = term % kWzRing;
-                    if (!(ok = wait(b, &b.wz_full[slot], (term / kWzRing) & 1))) break;
+                for (int k = 0; k < 3; ++k) {           // one term of the weighted Z after the other
+                    if (!(ok = wait(b, &b.wz_full[wz.slot], wz.phase))) break;
                     tc::tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_tmem_a(tmem + kColU, tmem + kColWz + 32 * slot + 8 * ks,
+                            mma_tmem_a(tmem + kColU, tmem + kColWz + 32 * wz.slot + 8 * ks,
                                        tc::desc_add(yd, ks * 2048), id_u, k + ks > 0);
-                        tc::mma_commit(&b.wz_empty[slot]);
+                        tc::mma_commit(&b.wz_empty[wz.slot]);
                         if (k == 2) {
                             tc::mma_commit(&b.u_full);
-                            tc::mma_commit(&b.empty[i % NS]);
+                            tc::mma_commit(&b.empty[at.slot]);
                         }
                     }
                     __syncwarp();
+                    wz.next();
                 }
+                at.next();
             }
         } else if (role == 1) {
             constexpr uint32_t id_sc = tc::idesc_bf16_f32(64, 64, 0, 0);
-            for (int i = 0; i < n; ++i) {
-                if (!(ok = tiles(i))) break;
-                if (i > 0 && !(ok = wait(b, &b.sc_empty, (i - 1) & 1))) break;
-                tc::tc_fence_after();
-                const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
-                const uint64_t yd = tc::smem_desc_sw128(stage(i), 16, 1024);
-                if (elect_one()) {
+            const uint64_t d0 = tc::smem_desc_sw128(tc::smem_u32(sm), 16, 1024);
+#pragma unroll 1
+            for (int i = 1 - NS; i < n; ++i) {
+                if (i >= 0) {
+                    if (!(ok = tiles(i))) break;
+                    if (i > 0 && !(ok = wait(b, &b.sc_empty, (i - 1) & 1))) break;
+                    tc::tc_fence_after();
+                    const uint64_t yd = tc::desc_add(d0, at.slot * S::STAGE), xd = tc::desc_add(yd, 2 * kTile);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
-                        tc::mma_bf16(tmem + kColSc, tc::desc_add(xd, off), tc::desc_add(yd, off), id_sc,
-                                     ks > 0);
+                        for (int ks = 0; ks < 8; ++ks) {
+                            const uint32_t off = (ks >> 2) * kBlock + (ks & 3) * 32;
+                            tc::mma_bf16(tmem + kColSc, tc::desc_add(xd, off), tc::desc_add(yd, off), id_sc,
+                                         ks > 0);
+                        }
+                        tc::mma_commit(&b.sc_full);
+                        tc::mma_commit(&b.empty[at.slot]);
                     }
-                    tc::mma_commit(&b.sc_full);
-                    tc::mma_commit(&b.empty[i % NS]);
+                    __syncwarp();
+                    at.next();
                 }
-                __syncwarp();
+                if (i + NS - 1 < n && !(ok = request(i + NS - 1))) break;
             }
         } else {
             constexpr uint32_t id_o1 = tc::idesc_bf16_f32(128, 64, 0, 0);
             constexpr uint32_t id_o2 = tc::idesc_bf16_f32(128, 64, 1, 0);
+            const uint64_t xd0 = tc::smem_desc_sw128(tc::smem_u32(sm) + 2 * kTile, 16, 1024);
+            const uint64_t zd0 = tc::smem_desc_sw128(tc::smem_u32(sm) + kTile, kBlock, 1024);
+            Ring<S::PBUF> pb;
+#pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 if (!(ok = tiles(i))) break;
                 if (i > 0 && !(ok = wait(b, &b.o_empty, (i - 1) & 1))) break;
                 // O1: the entering state read by X
                 if (!(ok = wait(b, &b.s_full, i & 1))) break;
                 tc::tc_fence_after();
-                const uint64_t xd = tc::smem_desc_sw128(stage(i) + 2 * kTile, 16, 1024);
+                const uint64_t xd = tc::desc_add(xd0, at.slot * S::STAGE);
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -872,33 +905,35 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 }
                 __syncwarp();
                 // O2: the chunk's own scores
-                const int buf = i % S::PBUF;
-                if (!(ok = wait(b, &b.p_full[buf], (i / S::PBUF) & 1))) break;
+                if (!(ok = wait(b, &b.p_full[pb.slot], pb.phase))) break;
                 tc::tc_fence_after();
-                const uint64_t zd = tc::smem_desc_sw128(stage(i) + kTile, kBlock, 1024);
+                const uint64_t zd = tc::desc_add(zd0, at.slot * S::STAGE);
                 if (elect_one()) {
 #pragma unroll 1
                     for (int q = 0; q < NP; ++q) {
                         const uint64_t pd =
-                            tc::smem_desc_sw128(tc::smem_u32(sP) + (buf * NP + q) * kBlock, 16, 1024);
+                            tc::smem_desc_sw128(tc::smem_u32(sP) + (pb.slot * NP + q) * kBlock, 16, 1024);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             tc::mma_bf16(tmem + kColO2, tc::desc_add(zd, ks * 2048),
                                          tc::desc_add(pd, ks * 32), id_o2, q + ks > 0);
                     }
-                    tc::mma_commit(&b.p_empty[buf]);
+                    tc::mma_commit(&b.p_empty[pb.slot]);
                     tc::mma_commit(&b.o_full);
-                    tc::mma_commit(&b.empty[i % NS]);
+                    tc::mma_commit(&b.empty[at.slot]);
                 }
                 __syncwarp();
+                pb.next();
+                at.next();
             }
         }
-        // every product has finished before the memory is given back
+        // every copy has landed and every product finished before the memory is given back
+#pragma unroll 1
+        for (int i = sent > NS ? sent - NS : 0; i < sent; ++i) wait(b, &b.full[i % NS], (i / NS) & 1);
         uint64_t* drain = &b.drain[role];
         if (elect_one()) tc::mma_commit(drain);
         __syncwarp();
-        const unsigned long long t0 = now_ns();
-        while (!poll(drain, 0) && now_ns() - t0 < kWaitNs) {}
+        wait(b, drain, 0);
         __syncwarp();
     }
     tc::tc_fence_before();
@@ -922,21 +957,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // [rows][T][heads][128] bf16 as {channel, head, token, row}; boxes of 64 channels x 64 tokens of
-// one head.  Tokens behind T read as zeros.  Stores: 32 channels, tokens behind T are not written.
+// one head.  Tokens behind T read as zeros.  Stores: 32 x 32, tokens behind T are not written.
 bool encode(CUtensorMap* m, const void* base, int heads, int T, int rows, bool store = false) {
     auto enc = encoder();
     if (!enc) return false;
     const cuuint64_t dims[4] = {D, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)rows};
     const cuuint64_t row = D * 2;
     const cuuint64_t strides[3] = {row, row * heads, row * heads * T};
-    const cuuint32_t box[4] = {store ? 32u : 64u, 1, (cuuint32_t)C, 1};
+    const cuuint32_t box[4] = {store ? 32u : 64u, 1, store ? 32u : (cuuint32_t)C, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NP, bool kSummary>
+template <int NP, bool kSummary, bool kF32>
 cudaError_t launch(const LaArgs& a, cudaStream_t s) {
     using S = TcShape<NP, kSummary>;
     TcArgs t;
@@ -948,10 +983,10 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
             !encode(&t.map[r][1], u.y, H / u.yg, a.sp.T, rows) ||
             !encode(&t.map[r][2], u.z, H / u.zg, a.sp.T, rows))
             return cudaErrorInvalidValue;
-        if (!kSummary && !u.out_f32 && !encode(&t.out[r], u.out, H, a.sp.T, rows, true))
+        if (!kSummary && !kF32 && !encode(&t.out[r], u.out, H, a.sp.T, rows, true))
             return cudaErrorInvalidValue;
     }
-    auto kern = la_tc_kernel<NP, kSummary>;
+    auto kern = la_tc_kernel<NP, kSummary, kF32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     kern<<<dim3((unsigned)(a.sp.units * H), a.runs), S::THREADS, S::SMEM, s>>>(t);
@@ -960,9 +995,13 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s) { return launch<1, true>(a, s); }
+cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s) {
+    return launch<1, true, false>(a, s);
+}
+// (the runs of one launch agree in out_f32, and have rows to multiply with where exact is set)
 cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s) {
-    return exact ? launch<3, false>(a, s) : launch<1, false>(a, s);
+    if (a.run[0].out_f32) return exact ? launch<3, false, true>(a, s) : launch<1, false, true>(a, s);
+    return exact ? launch<3, false, false>(a, s) : launch<1, false, false>(a, s);
 }
 
 // Read this file's status word (`stream` has finished) and clear it.
