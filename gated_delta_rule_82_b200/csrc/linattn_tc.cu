@@ -10,7 +10,7 @@
 // X, Y, Z arrive by TMA as 128-byte-swizzled tiles; one tile serves as K-major and as MN-major
 // operand.  The state lives in the registers of eight warps (a row of 64 channels per thread) and
 // goes to the tensor core as a bf16 operand through TMEM; the weighted Z as well, in three bf16
-// terms (24 bits, a ring of four 32-column slots), so that states are fp32-grade.  With NP = 3 the
+// terms (24 bits, 32 columns each), so that states are fp32-grade.  With NP = 3 the
 // scores and the state enter in three terms too (the state's second and third from shared memory).
 //
 // Roles (one CTA per SM, all of TMEM): warps 0-7 weight Z; 8-15 carry the state and write the
@@ -35,11 +35,11 @@ constexpr int C = kLaChunk;
 constexpr int D = 128;                    // contracted and output channels
 constexpr int kTile = C * D * 2;          // bytes of one operand tile
 constexpr int kBlock = C * 128;           // 64 channels of it
-constexpr int kGateRing = 4, kWzRing = 4;
+constexpr int kGateRing = 4;
 constexpr int kPolls = 1 << 18;
 
 // TMEM columns
-constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320, kColWz = 384;
+constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320;
 
 __device__ int g_la_status;               // 0, or kLaStatusWait since the host last read it
 
@@ -66,7 +66,7 @@ struct Ring {
 
 template <int NP, bool kSummary>
 struct TcShape {
-    static constexpr int STAGES = kSummary || NP == 1 ? 3 : 2;
+    static constexpr int STAGES = kSummary ? 4 : NP == 1 ? 3 : 2;
     static constexpr int STAGE = kSummary ? 2 * kTile : 3 * kTile;       // Y, Z, X
     static constexpr int PBUF = NP == 1 ? 2 : 1;                         // buffers of P
     static constexpr int P = kSummary ? 0 : PBUF * NP * kBlock;
@@ -77,13 +77,15 @@ struct TcShape {
     static constexpr int BARS = DOT + (kSummary ? 0 : 4 * C * 4);
     static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
     static constexpr int EXTRA = kSummary ? 16 : 20;                     // first of the single warps
-    static constexpr int THREADS = (EXTRA + (kSummary ? 2 : 4)) * 32;
+    static constexpr int THREADS = (EXTRA + (kSummary ? 3 : 4)) * 32;
+    static constexpr uint32_t WZ = kSummary ? 256 : 384;                  // its first column
+    static constexpr int UB = kSummary ? 2 : 1;      // buffers of U and of the weighted Z in TMEM
 };
 
 struct Bars {
-    uint64_t full[3], empty[3], gfull[kGateRing], gempty[kGateRing];
-    uint64_t sc_full, sc_empty, p_full[2], p_empty[2], wz_full[kWzRing], wz_empty[kWzRing];
-    uint64_t u_full, u_empty, s_full, s_empty, o_full, o_empty, dot_full, dot_empty, fin_full, tail, drain[3];
+    uint64_t full[4], empty[4], gfull[kGateRing], gempty[kGateRing];
+    uint64_t sc_full, sc_empty, p_full[2], p_empty[2], wz_full[2], wz_empty[2];
+    uint64_t u_full[2], u_empty[2], s_full, s_empty, o_full, o_empty, dot_full, dot_empty, fin_full, tail, drain[3];
     double fin[8];
     uint32_t tmem;
     volatile int abort;
@@ -282,18 +284,18 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             tc::mbar_init(&b.gfull[i], 1);
             tc::mbar_init(&b.gempty[i], S::EXTRA);    // every element warp
         }
-        for (int i = 0; i < kWzRing; ++i) {
+        for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&b.wz_full[i], 8);
             tc::mbar_init(&b.wz_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&b.p_full[i], 4);
             tc::mbar_init(&b.p_empty[i], 1);
         }
         tc::mbar_init(&b.sc_full, 1);
         tc::mbar_init(&b.sc_empty, 4);
-        tc::mbar_init(&b.u_full, 1);
-        tc::mbar_init(&b.u_empty, 8);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&b.u_full[i], 1);
+            tc::mbar_init(&b.u_empty[i], 8);
+        }
         tc::mbar_init(&b.s_full, 8);
         tc::mbar_init(&b.s_empty, 1);
         tc::mbar_init(&b.o_full, 1);
@@ -323,11 +325,11 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const int m = lane >> 3, e = warp >> 2;
         const uint32_t zat = ((m >> 1) * 8 + (lane & 7)) * 128 + (quarter >> 1) * kBlock +
                              ((((quarter & 1) * 4 + 2 * e + (m & 1)) ^ (lane & 7)) << 4);
-        const uint32_t to = tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColWz);
+        const uint32_t to = tc::tmem_addr(tmem, 32 * quarter + 16 * e, S::WZ);
         const bool packed = a.sp.cu != nullptr;
         Ring<NS> at;
         Ring<kGateRing> gp;
-        Ring<kWzRing> wz;
+        Ring<S::UB> wz;
         const uint32_t z0 = tc::smem_u32(sm) + kTile + zat;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
@@ -350,21 +352,19 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             arrive_warp(&b.gempty[gp.slot]);
             at.next();
             gp.next();
-            bool ok = true;
+            if (i >= S::UB && !wait(b, &b.wz_empty[wz.slot], wz.phase ^ 1)) break;
+            tc::tc_fence_after();
 #pragma unroll 1
             for (int k = 0; k < 3; ++k) {
-                if (3 * i + k >= kWzRing && !(ok = wait(b, &b.wz_empty[wz.slot], wz.phase ^ 1))) break;
-                tc::tc_fence_after();
                 uint32_t t[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) t[j] = cut2(v[j]);
-                tmem_st_16x32(to + 32 * wz.slot, t);
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                arrive_warp(&b.wz_full[wz.slot]);
-                wz.next();
+                tmem_st_16x32(to + 96 * wz.slot + 32 * k, t);
             }
-            if (!ok) break;
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            arrive_warp(&b.wz_full[wz.slot]);
+            wz.next();
         }
     } else if (warp < 16) {
         // ------------------------------------------ the state: 64 contracted channels of one row
@@ -450,11 +450,12 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             float2 dot[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) dot[j] = make_float2(0.f, 0.f);
-#pragma unroll 1
+            float2 x[8], y[8];
+            const uint32_t o1 = tc::tmem_addr(tmem, 32 * quarter, kColO1 + tq), o2 = o1 + (kColO2 - kColO1);
+            tmem_ld_16x32(o1, x);
+            tmem_ld_16x32(o2, y);
+#pragma unroll
             for (int e = 0; e < 2; ++e) {                        // 16 channels
-                float2 x[8], y[8];
-                tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO1 + tq), x);
-                tmem_ld_16x32(tc::tmem_addr(tmem, 32 * quarter + 16 * e, kColO2 + tq), y);
                 ld_wait(x, y);
                 if (e == 1) {
                     tc::tc_fence_before();
@@ -467,12 +468,12 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                     x[2 * j] = fma2(x[2 * j], w, y[2 * j]);
                     x[2 * j + 1] = fma2(x[2 * j + 1], w, y[2 * j + 1]);
                 }
+                const uint32_t at0 = tc::smem_u32(sOut) + stage_at(8 * (m4 >> 1) + (lane & 7), 2 * e + (m4 & 1));
                 if constexpr (dots) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {                // 16 tokens: four 8 x 8 matrices
                         uint32_t d[4];
-                        ldsm4t(d, tc::smem_u32(sOut) +
-                                      stage_at(16 * j + 8 * (m4 >> 1) + (lane & 7), 2 * e + (m4 & 1)));
+                        ldsm4t(d, at0 + 1024 * j);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             dot[2 * j + (k >> 1)] = fma2(x[4 * j + k], make_float2(lo_f(d[k]), hi_f(d[k])),
@@ -481,14 +482,15 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                     __syncwarp();
                 }
                 if constexpr (!kF32) {
+                    uint32_t o[8];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) o[k] = pack2(x[4 * j + k].x, x[4 * j + k].y);
-                        stsm4t(tc::smem_u32(sOut) +
-                                   stage_at(16 * j + 8 * (m4 >> 1) + (lane & 7), 2 * e + (m4 & 1)), o);
+                    for (int j = 0; j < 8; ++j) o[j] = pack2(x[j].x, x[j].y);
+                    if (e == 0) {                                // (in flight while this half is stored)
+                        tmem_ld_16x32(o1 + (16u << 16), x);
+                        tmem_ld_16x32(o2 + (16u << 16), y);
                     }
+                    stsm4t(at0, o);
+                    stsm4t(at0 + 1024, o + 4);
                 } else {
                     float* dst = static_cast<float*>(R.out) + ((size_t)tok * H + h) * D + ch0 + 16 * e + gr;
 #pragma unroll
@@ -497,6 +499,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                         float* at = dst + (size_t)t * H * D + 8 * (j & 1);
                         if (t < live) at[0] = x[j].x;
                         if (t + 1 < live) at[(size_t)H * D] = x[j].y;
+                    }
+                    if (e == 0) {
+                        tmem_ld_16x32(o1 + (16u << 16), x);
+                        tmem_ld_16x32(o2 + (16u << 16), y);
                     }
                 }
             }
@@ -561,28 +567,32 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
             return true;
         };
+        // In the order in which nothing is waited for: O1 and O2 of a chunk run beside the next
+        // update, and O1 of the next chunk beside the outputs of this one.
+        if constexpr (!kSummary) ok = put_state(0);
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < n && ok; ++i) {
             const int gs = i % kGateRing;
-            if constexpr (!kSummary)
-                if (!(ok = put_state(i))) break;
-            if (!(ok = wait(b, &b.gfull[gs], (i / kGateRing) & 1))) break;
-            const float2 total = make_float2(gates[gs].total, gates[gs].total);
-            if constexpr (kSummary) arrive_warp(&b.gempty[gs]);
-            if (!(ok = wait(b, &b.u_full, i & 1))) break;
+            const int ub = kSummary ? i & 1 : 0;
+            if (!(ok = wait(b, &b.u_full[ub], (kSummary ? i >> 1 : i) & 1))) break;
             tc::tc_fence_after();
+            // (U was formed from the chunk's decays: they are there)
+            const float2 total = make_float2(gates[gs].total, gates[gs].total);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float x[16];
-                tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + col0 + 16 * q), x);
+                tc::tmem_ld16_sync(tc::tmem_addr(tmem, 32 * quarter, kColU + D * ub + col0 + 16 * q), x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     st[8 * q + j] = fma2(st[8 * q + j], total, make_float2(x[2 * j], x[2 * j + 1]));
             }
             tc::tc_fence_before();
-            arrive_warp(&b.u_empty);
-            if constexpr (!kSummary)
+            arrive_warp(&b.u_empty[ub]);
+            if constexpr (kSummary) arrive_warp(&b.gempty[gs]);
+            if constexpr (!kSummary) {
+                if (i + 1 < n && !(ok = put_state(i + 1))) break;
                 if (!(ok = put_out(i))) break;
+            }
         }
         if (!kSummary && lane == 0) tc::bulk_wait_all();
         if (ok) {
@@ -814,37 +824,37 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             return true;
         };
         bool ok = true;
-        if (kSummary || role == 0) {
+        if (role == 0) {
             constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 128, 0, 1);
             const uint64_t yd0 = tc::smem_desc_sw128(tc::smem_u32(sm), kBlock, 1024);
-            Ring<kWzRing> wz;
+            Ring<S::UB> ub;
 #pragma unroll 1
-            for (int i = kSummary ? 1 - NS : 0; i < n && ok; ++i) {
-                if (kSummary && i + NS - 1 < n && !(ok = request(i + NS - 1))) break;
-                if (kSummary && i < 0) continue;
+            for (int i = 0; i < n; ++i) {
                 if (!(ok = tiles(i))) break;
-                if (i > 0 && !(ok = wait(b, &b.u_empty, (i - 1) & 1))) break;
+                if (i >= S::UB && !(ok = wait(b, &b.u_empty[ub.slot], ub.phase ^ 1))) break;
                 const uint64_t yd = tc::desc_add(yd0, at.slot * S::STAGE);
+                if (!(ok = wait(b, &b.wz_full[ub.slot], ub.phase))) break;
+                tc::tc_fence_after();
+                if (elect_one()) {
 #pragma unroll 1
-                for (int k = 0; k < 3; ++k) {           // one term of the weighted Z after the other
-                    if (!(ok = wait(b, &b.wz_full[wz.slot], wz.phase))) break;
-                    tc::tc_fence_after();
-                    if (elect_one()) {
+                    for (int k = 0; k < 3; ++k)         // one term of the weighted Z after the other
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_tmem_a(tmem + kColU, tmem + kColWz + 32 * wz.slot + 8 * ks,
+                            mma_tmem_a(tmem + kColU + D * ub.slot,
+                                       tmem + S::WZ + 96 * ub.slot + 32 * k + 8 * ks,
                                        tc::desc_add(yd, ks * 2048), id_u, k + ks > 0);
-                        tc::mma_commit(&b.wz_empty[wz.slot]);
-                        if (k == 2) {
-                            tc::mma_commit(&b.u_full);
-                            tc::mma_commit(&b.empty[at.slot]);
-                        }
-                    }
-                    __syncwarp();
-                    wz.next();
+                    tc::mma_commit(&b.wz_empty[ub.slot]);
+                    tc::mma_commit(&b.u_full[ub.slot]);
+                    tc::mma_commit(&b.empty[at.slot]);
                 }
+                __syncwarp();
                 at.next();
+                ub.next();
             }
+        } else if (kSummary) {
+#pragma unroll 1
+            for (int i = 0; i < n; ++i)
+                if (!(ok = request(i))) break;
         } else if (role == 1) {
             constexpr uint32_t id_sc = tc::idesc_bf16_f32(64, 64, 0, 0);
             const uint64_t d0 = tc::smem_desc_sw128(tc::smem_u32(sm), 16, 1024);
