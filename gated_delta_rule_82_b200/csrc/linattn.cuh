@@ -150,13 +150,11 @@ inline size_t la_chunk_ids(long long tokens, int n) { return (size_t)(tokens / k
 // log2 of a token's decay.  exp(g) below 2^-160 is zero in fp32; the floor keeps -inf (a reset)
 // out of the differences.
 constexpr double kLaMinLog2 = -160.0;
-__device__ __forceinline__ double log2_decay(float g) {
-    const double x = (double)g * 1.4426950408889634;
-    return x < kLaMinLog2 ? kLaMinLog2 : x;     // (NaN stays NaN)
-}
 __device__ __forceinline__ double log2_decay(const float* g, int per_token, long long tok, int H,
                                              int h, bool live) {
-    return live ? log2_decay(per_token ? g[(size_t)tok * H + h] : g[h]) : 0.0;
+    if (!live) return 0.0;
+    const double x = (double)(per_token ? g[(size_t)tok * H + h] : g[h]) * 1.4426950408889634;
+    return x < kLaMinLog2 ? kLaMinLog2 : x;     // (NaN stays NaN)
 }
 
 // Tokens per unit for sequences of `total` tokens (the longest `longest`) over H heads.

@@ -49,9 +49,14 @@ struct TcArgs {
     CUtensorMap out[kLaMaxRuns];          // bf16 outputs
 };
 
+// A chunk's decays, as log2 sums over its 16-token blocks that start or end at a block's edge, so
+// that no two long sums are subtracted: the decay between two tokens of different blocks is
+// r (to the end of the block) + whole blocks + l (from the start of the block).
 struct GateSlot {
-    float hi[C], lo[C], out[C], upd[C];
-    float total, pad[7];
+    float l[C], r[C];        // up to and including the token; behind the token
+    float out[C], upd[C];    // weights of the read-out and of the update, with their scales
+    float block[4];          // whole blocks
+    float total, pad[3];     // exp2 of the chunk's sum
 };
 
 // Position in a ring of N slots: the slot, and the parity of the phase that its n-th use completes.
@@ -70,11 +75,11 @@ struct TcShape {
     static constexpr int STAGE = kSummary ? 2 * kTile : 3 * kTile;       // Y, Z, X
     static constexpr int PBUF = NP == 1 ? 2 : 1;                         // buffers of P
     static constexpr int P = kSummary ? 0 : PBUF * NP * kBlock;
-    static constexpr int OUT = kSummary ? 0 : kTile;                     // outputs on their way out
+    static constexpr int OUT = kSummary ? 0 : 2 * kTile;                 // outputs on their way out
     static constexpr int SLO = kSummary ? 0 : (NP - 1) * D * D * 2;      // lower terms of the state
     static constexpr int GATES = STAGES * STAGE + P + SLO + OUT;
     static constexpr int DOT = GATES + kGateRing * (int)sizeof(GateSlot);
-    static constexpr int BARS = DOT + (kSummary ? 0 : 4 * C * 4);
+    static constexpr int BARS = DOT + (NP > 1 ? kGateRing * 4 * C * 4 : 0);
     static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
     static constexpr int EXTRA = kSummary ? 16 : 20;                     // first of the single warps
     static constexpr int THREADS = (EXTRA + (kSummary ? 3 : 4)) * 32;
@@ -85,7 +90,7 @@ struct TcShape {
 struct Bars {
     uint64_t full[4], empty[4], gfull[kGateRing], gempty[kGateRing];
     uint64_t sc_full, sc_empty, p_full[2], p_empty[2], wz_full[2], wz_empty[2];
-    uint64_t u_full[2], u_empty[2], s_full, s_empty, o_full, o_empty, dot_full, dot_empty, fin_full, tail, drain[3];
+    uint64_t u_full[2], u_empty[2], s_full, s_empty, o_full, o_empty, dot_full[kGateRing], dot_empty[kGateRing], fin_full, tail, drain[3];
     double fin[8];
     uint32_t tmem;
     volatile int abort;
@@ -147,6 +152,12 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, u
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// log2 of a decay exp(g), floored as kLaMinLog2 (a NaN stays one)
+__device__ __forceinline__ float log2_decay(float g) {
+    const float x = g * 1.44269504f;
+    return x < (float)kLaMinLog2 ? (float)kLaMinLog2 : x;
 }
 
 // ---- two fp32 values at a time
@@ -283,6 +294,8 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int i = 0; i < kGateRing; ++i) {
             tc::mbar_init(&b.gfull[i], 1);
             tc::mbar_init(&b.gempty[i], S::EXTRA);    // every element warp
+            tc::mbar_init(&b.dot_full[i], 8);
+            tc::mbar_init(&b.dot_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&b.wz_full[i], 8);
@@ -300,8 +313,6 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         tc::mbar_init(&b.s_empty, 1);
         tc::mbar_init(&b.o_full, 1);
         tc::mbar_init(&b.o_empty, 8);
-        tc::mbar_init(&b.dot_full, 8);
-        tc::mbar_init(&b.dot_empty, 1);
         tc::mbar_init(&b.fin_full, 8);
         tc::mbar_init(&b.tail, 1);
         for (int i = 0; i < 3; ++i) tc::mbar_init(&b.drain[i], 1);
@@ -423,28 +434,35 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const int ch0 = 32 * quarter, tq = 32 * half;
         const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
         const int m4 = lane >> 3;                                // matrix of an x4 access
-        uint8_t* sOut = sSlo + S::SLO + (warp - 8) * (kTile / 8);
+        uint8_t* sOut0 = sSlo + S::SLO + (warp - 8) * (kTile / 8);      // two areas, a tile apart
         constexpr bool dots = !kSummary && NP > 1;
-        const float o_scale = R.o_scale;
+        // The rows that the outputs are multiplied with, into the staging area, long before their use.
+        auto fetch_rows = [&](int i) {
+            const int Hd = H / R.dg, live = live_of(i) - tq;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.dot) +
+                                       ((size_t)(u.tok + chunk_at(i) * C + tq) * Hd + h / R.dg) * D + ch0 + 8 * tp;
+            uint8_t* sOut = sOut0 + (i & 1) * kTile;
+            if (lane == 0) tc::bulk_wait_read<1>();              // (what was last stored from it)
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 8 * k + tr;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             ::"r"(tc::smem_u32(sOut + stage_at(t, tp))),
+                               "l"(src + (t < live ? (size_t)t * Hd * D : 0)), "r"(t < live ? 16 : 0) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
         auto put_out = [&](int i) {
             const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i) - tq;
             const long long tok = u.tok + (long long)c * C + tq;
-            if (lane == 0) tc::bulk_wait_read_all();             // the staging area is free again
-            __syncwarp();
+            uint8_t* sOut = sOut0 + (i & 1) * kTile;
             if constexpr (dots) {
-                // the rows that the outputs are multiplied with, into the staging area
-                const int Hd = H / R.dg;
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.dot) +
-                                           ((size_t)tok * Hd + h / R.dg) * D + ch0 + 8 * tp;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = 8 * k + tr;
-                    uint4 w = make_uint4(0, 0, 0, 0);
-                    if (t < live) w = __ldg(reinterpret_cast<const uint4*>(src + (size_t)t * Hd * D));
-                    *reinterpret_cast<uint4*>(sOut + stage_at(t, tp)) = w;
-                }
-                __syncwarp();
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            } else if (lane == 0) {
+                tc::bulk_wait_read<1>();                         // the staging area is free again
             }
+            __syncwarp();
             if (!wait(b, &b.o_full, i & 1)) return false;
             tc::tc_fence_after();
             float2 dot[4];
@@ -463,8 +481,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 g = *reinterpret_cast<const float2*>(gates[gs].out + tq + 8 * j + gc);
-                    const float2 w = mul2(g, make_float2(o_scale, o_scale));
+                    const float2 w = *reinterpret_cast<const float2*>(gates[gs].out + tq + 8 * j + gc);
                     x[2 * j] = fma2(x[2 * j], w, y[2 * j]);
                     x[2 * j + 1] = fma2(x[2 * j + 1], w, y[2 * j + 1]);
                 }
@@ -539,31 +556,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                     }
                 dot[0].x += __shfl_xor_sync(0xffffffffu, dot[0].x, 4);
                 dot[0].y += __shfl_xor_sync(0xffffffffu, dot[0].y, 4);
-                if (i > 0 && !wait(b, &b.dot_empty, (i - 1) & 1)) return false;
+                if (i >= kGateRing && !wait(b, &b.dot_empty[gs], (i / kGateRing - 1) & 1)) return false;
                 if (!(lane & 4))
-                    *reinterpret_cast<float2*>(sDot + quarter * C + tq + 8 * (lane >> 3) + gc) = dot[0];
-                arrive_warp(&b.dot_full);
-                if (warp == 8) {
-                    if (!wait(b, &b.dot_full, i & 1)) return false;
-                    const int all = live_of(i);
-                    const long long t0 = u.tok + (long long)c * C;
-                    double sum = 0.0;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = 32 * e + lane;
-                        const float s = (sDot[t] + sDot[C + t]) + (sDot[2 * C + t] + sDot[3 * C + t]);
-                        if (t < all) {
-                            R.dot_out[(size_t)(t0 + t) * H + h] = s;
-                            sum += (double)s;
-                        }
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0)
-                        R.dot_sum[(size_t)la_chunk_id(u.tok - (long long)u.index * a.sp.L, u.seq,
-                                                      u.index * (a.sp.L / C) + c) * H + h] = sum;
-                    arrive_warp(&b.dot_empty);
-                }
+                    *reinterpret_cast<float2*>(sDot + (4 * gs + quarter) * C + tq + 8 * (lane >> 3) + gc) = dot[0];
+                arrive_warp(&b.dot_full[gs]);
             }
             return true;
         };
@@ -573,6 +569,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
             const int gs = i % kGateRing;
+            if constexpr (dots) fetch_rows(i);
             const int ub = kSummary ? i & 1 : 0;
             if (!(ok = wait(b, &b.u_full[ub], (kSummary ? i >> 1 : i) & 1))) break;
             tc::tc_fence_after();
@@ -654,15 +651,15 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1)) return false;
             const GateSlot& g = gates[gs];
             const int r0 = 16 * quarter + gr;
-            const float rh[2] = {g.hi[r0], g.hi[r0 + 8]}, rl[2] = {g.lo[r0], g.lo[r0 + 8]};
             // Tiles off the diagonal: the decay between row and column passes the edge of this
-            // warp's 16 rows, exp(G_i - G_j) = exp(G_i - edge) exp(edge - G_j), both at most one.
-            const int edge = rev ? 16 * quarter + 15 : 16 * quarter - 1;
-            const float eh = edge >= 0 ? g.hi[edge] : 0.f, el = edge >= 0 ? g.lo[edge] : 0.f;
-            const float sg = rev ? -1.f : 1.f;
+            // warp's 16 rows, so it is a row factor times a column factor, both at most one.
+            const float* edge = rev ? g.r : g.l;
+            const float* far = rev ? g.l : g.r;
             float ra[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) ra[e] = ex2(sg * ((rh[e] - eh) + (rl[e] - el))) * p_scale;
+            for (int e = 0; e < 2; ++e) ra[e] = ex2(edge[r0 + 8 * e]) * p_scale;
+            const float rl[2] = {g.l[r0], g.l[r0 + 8]};
+            const float sg = rev ? -1.f : 1.f;
             if (!wait(b, &b.sc_full, i & 1)) return false;
             if (i >= PB && !wait(b, &b.p_empty[buf], (i / PB - 1) & 1)) return false;
             tc::tc_fence_after();
@@ -670,43 +667,41 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             uint8_t* p = sP + buf * NP * kBlock + r0 * 128 + gc * 2;
             float2 x[4], nx[4];
             tmem_ld_16x16(sc + 16 * quarter, x);
-            // the diagonal tile, while the first of the others is on its way
-            int t = rev ? 3 : 0;
-            const int dt = rev ? -1 : 1;
+            // the diagonal tile, while the first of the others is on its way (outwards from it)
+            const int dt = rev ? 1 : -1, end = rev ? 4 : -1;
+            int t = quarter + dt;
+            float mid = 0.f;                                     // whole blocks in between
             tmem_ld_wait4(x);
-            if (t != quarter) tmem_ld_16x16(sc + 16 * t, nx);
+            if (t != end) tmem_ld_16x16(sc + 16 * t, nx);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = 16 * quarter + 8 * j + gc;
-                const float2 ch = *reinterpret_cast<const float2*>(g.hi + c);
-                const float2 cl = *reinterpret_cast<const float2*>(g.lo + c);
+                const float2 cl = *reinterpret_cast<const float2*>(g.l + c);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = r0 + 8 * e;
-                    const float d0 = (rh[e] - ch.x) + (rl[e] - cl.x), d1 = (rh[e] - ch.y) + (rl[e] - cl.y);
                     float2& w = x[2 * j + e];
-                    w.x = (rev ? row <= c : row >= c) ? w.x * ex2(sg * d0) * p_scale : 0.f;
-                    w.y = (rev ? row <= c + 1 : row >= c + 1) ? w.y * ex2(sg * d1) * p_scale : 0.f;
+                    w.x = (rev ? row <= c : row >= c) ? w.x * ex2(sg * (rl[e] - cl.x)) * p_scale : 0.f;
+                    w.y = (rev ? row <= c + 1 : row >= c + 1) ? w.y * ex2(sg * (rl[e] - cl.y)) * p_scale : 0.f;
                 }
             }
             put(p, 16 * quarter, x);
 #pragma unroll 1
-            for (; t != quarter; t += dt) {
+            for (; t != end; t += dt) {
                 tmem_ld_wait4(nx);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = nx[j];
-                if (t + dt != quarter) tmem_ld_16x16(sc + 16 * (t + dt), nx);
+                if (t + dt != end) tmem_ld_16x16(sc + 16 * (t + dt), nx);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int c = 16 * t + 8 * j + gc;
-                    const float2 ch = *reinterpret_cast<const float2*>(g.hi + c);
-                    const float2 cl = *reinterpret_cast<const float2*>(g.lo + c);
-                    const float2 cb = make_float2(ex2(sg * ((eh - ch.x) + (el - cl.x))),
-                                                  ex2(sg * ((eh - ch.y) + (el - cl.y))));
+                    const float2 cf = *reinterpret_cast<const float2*>(far + c);
+                    const float2 cb = make_float2(ex2(cf.x + mid), ex2(cf.y + mid));
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         x[2 * j + e] = mul2(mul2(x[2 * j + e], cb), make_float2(ra[e], ra[e]));
                 }
+                mid += g.block[t];
                 put(p, 16 * t, x);
             }
             tc::tc_fence_before();
@@ -720,7 +715,32 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (!make_p(i)) break;
     } else if (warp == S::EXTRA) {
         // -------------------------------------------------------------------------- the decays
-        const float u_scale = R.u_scale;
+        // (and the output rows' products: their sums over the channel groups, and over the chunk)
+        constexpr bool dots = !kSummary && NP > 1;
+        auto dot_rows = [&](int i) {
+            const int slot = i % kGateRing;
+            const float* d = sDot + 4 * slot * C;
+            if (!wait(b, &b.dot_full[slot], (i / kGateRing) & 1)) return false;
+            const int c = chunk_at(i), live = live_of(i);
+            const long long tok = u.tok + (long long)c * C;
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 32 * e + lane;
+                const float s = (d[t] + d[C + t]) + (d[2 * C + t] + d[3 * C + t]);
+                if (t < live) {
+                    R.dot_out[(size_t)(tok + t) * H + h] = s;
+                    sum += s;
+                }
+            }
+            arrive_warp(&b.dot_empty[slot]);
+            sum = warp_sum(sum);
+            if (lane == 0)
+                R.dot_sum[(size_t)la_chunk_id(u.tok - (long long)u.index * a.sp.L, u.seq,
+                                              u.index * (a.sp.L / C) + c) * H + h] = (double)sum;
+            return true;
+        };
+        const float u_scale = R.u_scale, o_scale = R.o_scale;
         // The raw decays are requested a chunk ahead (and stay requested there: volatile), clamped to
         // the unit and unconditional, so that nothing depends on them before they are used.
         const float* gp = a.g + h + (a.per_token ? (size_t)u.tok * H : 0);
@@ -737,37 +757,54 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             const int gs = i % kGateRing, live = live_of(i);
             t0 = chunk_at(min(i + 1, n - 1)) * C + 2 * lane;
             next = make_float2(load(t0), load(t0 + 1));
-            const double g0 = 2 * lane < live ? log2_decay(cur.x) : 0.0;
-            const double g1 = 2 * lane + 1 < live ? log2_decay(cur.y) : 0.0;
-            double s = g0 + g1;
+            const float g0 = 2 * lane < live ? log2_decay(cur.x) : 0.f;
+            const float g1 = 2 * lane + 1 < live ? log2_decay(cur.y) : 0.f;
+            float pre = g0 + g1, suf = pre;                       // over the 8 lanes of a block
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += x;
+            for (int o = 1; o < 8; o <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, pre, o, 8), y = __shfl_down_sync(0xffffffffu, suf, o, 8);
+                if ((lane & 7) >= o) pre += x;
+                if ((lane & 7) + o < 8) suf += y;
             }
-            const double all = __shfl_sync(0xffffffffu, s, 31);
-            if constexpr (kSummary) decay += all;
-            const double G[2] = {s - g1, s};
+            float before = __shfl_up_sync(0xffffffffu, pre, 1, 8), after = __shfl_down_sync(0xffffffffu, suf, 1, 8);
+            if ((lane & 7) == 0) before = 0.f;
+            if ((lane & 7) == 7) after = 0.f;
+            float blk[4], ahead = 0.f, behind = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                blk[k] = __shfl_sync(0xffffffffu, pre, 8 * k + 7);
+                ahead += k < (lane >> 3) ? blk[k] : 0.f;
+                behind += k > (lane >> 3) ? blk[k] : 0.f;
+            }
+            const float all = (blk[0] + blk[1]) + (blk[2] + blk[3]);
+            if constexpr (kSummary) decay += (double)all;
             if (i >= kGateRing && !wait(b, &b.gempty[gs], (i / kGateRing - 1) & 1)) break;
             GateSlot& g = gates[gs];
-            float up[2], down[2], hi[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                hi[e] = (float)G[e];
-                lo[e] = (float)(G[e] - (double)hi[e]);
-                down[e] = ex2(hi[e]);
-                up[e] = ex2((float)(all - G[e]));
-            }
+            const float2 l = make_float2(before + g0, pre), r = make_float2(g1 + after, after);
+            const float2 down = make_float2(ex2(ahead + l.x), ex2(ahead + l.y));     // since the start
+            const float2 up = make_float2(ex2(r.x + behind), ex2(r.y + behind));     // to the end
+            const float2 w = rev ? down : up;
             const int t = 2 * lane;
-            *reinterpret_cast<float2*>(g.hi + t) = make_float2(hi[0], hi[1]);
-            *reinterpret_cast<float2*>(g.lo + t) = make_float2(lo[0], lo[1]);
-            *reinterpret_cast<float2*>(g.out + t) = rev ? make_float2(up[0], up[1]) : make_float2(down[0], down[1]);
             *reinterpret_cast<float2*>(g.upd + t) =
-                make_float2(t < live ? (rev ? down[0] : up[0]) * u_scale : 0.f,
-                            t + 1 < live ? (rev ? down[1] : up[1]) * u_scale : 0.f);
-            if (lane == 0) g.total = ex2((float)all);
+                make_float2(t < live ? w.x * u_scale : 0.f, t + 1 < live ? w.y * u_scale : 0.f);
+            if constexpr (!kSummary) {
+                *reinterpret_cast<float2*>(g.l + t) = l;
+                *reinterpret_cast<float2*>(g.r + t) = r;
+                const float2 o = rev ? up : down;
+                *reinterpret_cast<float2*>(g.out + t) = make_float2(o.x * o_scale, o.y * o_scale);
+            }
+            if (lane == 0) {
+                g.total = ex2(all);
+                *reinterpret_cast<float4*>(g.block) = make_float4(blk[0], blk[1], blk[2], blk[3]);
+            }
             arrive_warp(&b.gfull[gs]);
+            // (three chunks behind, so that the element warps never wait for this)
+            if constexpr (dots)
+                if (i >= 3 && !dot_rows(i - 3)) break;
         }
+        if constexpr (dots)
+            for (int i = max(n - 3, 0); i < n; ++i)
+                if (!dot_rows(i)) break;
         if (kSummary && lane == 0) R.unit_decay[(size_t)unit * H + h] = decay;
     } else {
         // ---------------------------------------------- tcgen05.mma: U (+ 1), Sc (+ 2), O (+ 3)
