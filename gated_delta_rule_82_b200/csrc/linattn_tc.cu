@@ -874,12 +874,12 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 tc::tc_fence_after();
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int k = 0; k < 3; ++k)         // one term of the weighted Z after the other
-#pragma unroll
+                    for (int k = 2; k >= 0; --k)        // the smallest term of the weighted Z first:
+#pragma unroll                                          // fewer roundings at the full size
                         for (int ks = 0; ks < 4; ++ks)
                             mma_tmem_a(tmem + kColU + D * ub.slot,
                                        tmem + S::WZ + 96 * ub.slot + 32 * k + 8 * ks,
-                                       tc::desc_add(yd, ks * 2048), id_u, k + ks > 0);
+                                       tc::desc_add(yd, ks * 2048), id_u, k < 2 || ks > 0);
                     tc::mma_commit(&b.wz_empty[ub.slot]);
                     tc::mma_commit(&b.u_full[ub.slot]);
                     tc::mma_commit(&b.empty[at.slot]);
@@ -932,22 +932,24 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 tc::tc_fence_after();
                 const uint64_t xd = tc::desc_add(xd0, at.slot * S::STAGE);
                 if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_tmem_a(tmem + kColO1, tmem + kColS + 8 * ks,
-                                   tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, ks > 0);
                     if constexpr (NP > 1) {
 #pragma unroll 1
-                        for (int q = 0; q < NP - 1; ++q) {
+                        for (int q = NP - 2; q >= 0; --q) {
                             const uint64_t sd =
                                 tc::smem_desc_sw128(tc::smem_u32(sSlo) + q * D * D * 2, 16, 1024);
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks)
                                 tc::mma_bf16(tmem + kColO1,
                                              tc::desc_add(sd, (ks >> 2) * (D * 128) + (ks & 3) * 32),
-                                             tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, 1);
+                                             tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1,
+                                             q < NP - 2 || ks > 0);
                         }
                     }
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_tmem_a(tmem + kColO1, tmem + kColS + 8 * ks,
+                                   tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1,
+                                   NP > 1 || ks > 0);
                     tc::mma_commit(&b.s_empty);
                 }
                 __syncwarp();
@@ -957,13 +959,13 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 const uint64_t zd = tc::desc_add(zd0, at.slot * S::STAGE);
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int q = 0; q < NP; ++q) {
+                    for (int q = NP - 1; q >= 0; --q) {
                         const uint64_t pd =
                             tc::smem_desc_sw128(tc::smem_u32(sP) + (pb.slot * NP + q) * kBlock, 16, 1024);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             tc::mma_bf16(tmem + kColO2, tc::desc_add(zd, ks * 2048),
-                                         tc::desc_add(pd, ks * 32), id_o2, q + ks > 0);
+                                         tc::desc_add(pd, ks * 32), id_o2, q < NP - 1 || ks > 0);
                     }
                     tc::mma_commit(&b.p_empty[pb.slot]);
                     tc::mma_commit(&b.o_full);
