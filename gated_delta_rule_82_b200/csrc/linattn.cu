@@ -153,18 +153,21 @@ __device__ __forceinline__ void load_rows(__nv_bfloat16* dst, const T* src, long
     }
 }
 
-// acc += A B over the pairs of terms whose product is not below the precision kept.
+// acc += A B for the leading terms, low += A B for the other pairs whose product is not below the
+// precision kept.  Two accumulators, because the tensor core's sums do not round to nearest: what
+// is lost then is a part of the few leading products only.
 template <int NA, int NB>
-__device__ __forceinline__ void mma_terms(float acc[4], const uint32_t (*a)[4],
+__device__ __forceinline__ void mma_terms(float acc[4], float low[4], const uint32_t (*a)[4],
                                           const uint32_t (*b)[2]) {
     constexpr int N = NA > NB ? NA : NB;
 #pragma unroll
-    for (int s = N - 1; s >= 0; --s)     // smallest terms first
+    for (int s = N - 1; s > 0; --s)      // smallest terms first
 #pragma unroll
         for (int i = 0; i < NA; ++i) {
             const int j = s - i;
-            if (j >= 0 && j < NB) mma(acc, a[i], b[j][0], b[j][1]);
+            if (j >= 0 && j < NB) mma(low, a[i], b[j][0], b[j][1]);
         }
+    mma(acc, a[0], b[0][0], b[0][1]);
 }
 
 template <typename T, int DC, int DO, bool kSummary, int NP>
@@ -212,6 +215,10 @@ la_run_kernel(const LaArgs a) {
         const int left = u.len - c * C;
         *g0 = log2_decay(a.g, a.per_token, tok + 2 * lane, H, h, 2 * lane < left);
         *g1 = log2_decay(a.g, a.per_token, tok + 2 * lane + 1, H, h, 2 * lane + 1 < left);
+    };
+
+    auto load_z = [&](uint32_t f[4], const __nv_bfloat16* z, int kk) {
+        ldsm4t(f, smem_addr(z + (kk * 16 + (lane >> 4) * 8 + (lane & 7)) * LO + r0 + ((lane >> 3) & 1) * 8));
     };
 
     // The state: rows r0 + gr (+ 8), columns 8 n + gc (+ 1).
@@ -263,13 +270,13 @@ la_run_kernel(const LaArgs a) {
         const __nv_bfloat16* sZ = sY + NI * S::XY;
         const __nv_bfloat16* sX = sZ + NI * S::Z;
 
-        float acc[4][2][4];
+        float acc[4][2][4], low[4][2][4];     // (low stays zero, and free, without lower terms)
         if constexpr (!kSummary) {
             // 1. this warp's tiles of P (16 x 16; on the kept side of the diagonal)
             for (int t = warp; t < 16; t += NW) {
                 const int mi = t & 3, nj = t >> 2;
                 if (rev ? mi > nj : mi < nj) continue;
-                float p[2][4] = {};
+                float p[2][4] = {}, pl[2][4] = {};
 #pragma unroll
                 for (int kk = 0; kk < KC; ++kk) {
                     uint32_t fa[NI][4], fb[NI][4];
@@ -289,7 +296,7 @@ la_run_kernel(const LaArgs a) {
                             b[q][0] = fb[q][2 * n];
                             b[q][1] = fb[q][2 * n + 1];
                         }
-                        mma_terms<NI, NI>(p[n], fa, b);
+                        mma_terms<NI, NI>(p[n], pl[n], fa, b);
                     }
                 }
 #pragma unroll
@@ -303,7 +310,7 @@ la_run_kernel(const LaArgs a) {
                             const float d = (gb.hi[row] - gb.hi[col + e]) +
                                             (gb.lo[row] - gb.lo[col + e]);
                             const bool keep = rev ? row <= col + e : row >= col + e;
-                            w[e] = keep ? p[n][2 * e2 + e] * exp2f(rev ? -d : d) * R.p_scale : 0.f;
+                            w[e] = keep ? (p[n][2 * e2 + e] + pl[n][2 * e2 + e]) * exp2f(rev ? -d : d) * R.p_scale : 0.f;
                         }
                         uint32_t t3[NP];
                         split2<NP>(w[0], w[1], t3);
@@ -318,7 +325,7 @@ la_run_kernel(const LaArgs a) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[m][n][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) acc[m][n][e] = low[m][n][e] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < KC; ++kk) {
                 uint32_t b[2][NP][2];
@@ -337,8 +344,8 @@ la_run_kernel(const LaArgs a) {
                     for (int q = 0; q < NI; ++q)
                         ldsm4(fa[q], smem_addr(sX + q * S::XY + (m * 16 + (lane & 15)) * LC +
                                                kk * 16 + (lane >> 4) * 8));
-                    mma_terms<NI, NP>(acc[m][0], fa, b[0]);
-                    mma_terms<NI, NP>(acc[m][1], fa, b[1]);
+                    mma_terms<NI, NP>(acc[m][0], low[m][0], fa, b[0]);
+                    mma_terms<NI, NP>(acc[m][1], low[m][1], fa, b[1]);
                 }
             }
 #pragma unroll
@@ -350,31 +357,24 @@ la_run_kernel(const LaArgs a) {
                     for (int n = 0; n < 2; ++n) {
                         acc[m][n][2 * e2] *= w;
                         acc[m][n][2 * e2 + 1] *= w;
+                        low[m][n][2 * e2] *= w;
+                        low[m][n][2 * e2 + 1] *= w;
                     }
                 }
             __syncthreads();              // P is complete
         }
-        // 3. the chunk's own products, and the state update, 16 tokens of z at a time
-        const float total = gb.total;
+        if constexpr (!kSummary) {
+            // 3. the chunk's own products, 16 tokens of z at a time.  z^T tile: registers 0, 2 are
+            // channels 0-7, 1, 3 channels 8-15; 2, 3 tokens 8-15
 #pragma unroll
-        for (int n = 0; n < DC / 8; ++n)
+            for (int kk = 0; kk < C / 16; ++kk) {
+                uint32_t fz[NI][4], b[2][NI][2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) M[n][e] *= total;
-#pragma unroll
-        for (int kk = 0; kk < C / 16; ++kk) {
-            // z^T tile: registers 0, 2 are channels 0-7, 1, 3 channels 8-15; 2, 3 tokens 8-15
-            uint32_t fz[NI][4];
-#pragma unroll
-            for (int q = 0; q < NI; ++q)
-                ldsm4t(fz[q], smem_addr(sZ + q * S::Z +
-                                        (kk * 16 + (lane >> 4) * 8 + (lane & 7)) * LO + r0 +
-                                        ((lane >> 3) & 1) * 8));
-            if constexpr (!kSummary) {
-                uint32_t b[2][NI][2];
-#pragma unroll
-                for (int q = 0; q < NI; ++q)
+                for (int q = 0; q < NI; ++q) {
+                    load_z(fz[q], sZ + q * S::Z, kk);
 #pragma unroll
                     for (int n = 0; n < 2; ++n) { b[n][q][0] = fz[q][n]; b[n][q][1] = fz[q][n + 2]; }
+                }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     if (rev ? m > kk : m < kk) continue;
@@ -383,36 +383,8 @@ la_run_kernel(const LaArgs a) {
                     for (int q = 0; q < NP; ++q)
                         ldsm4(fp[q], smem_addr(sP + q * C * LP + (m * 16 + (lane & 15)) * LP +
                                                kk * 16 + (lane >> 4) * 8));
-                    mma_terms<NP, NI>(acc[m][0], fp, b[0]);
-                    mma_terms<NP, NI>(acc[m][1], fp, b[1]);
-                }
-            }
-            uint32_t wz[NU][4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = kk * 16 + gc + (r >> 1) * 8;
-                float v0 = 0.f, v1 = 0.f;
-#pragma unroll
-                for (int q = NI - 1; q >= 0; --q) { v0 += lo_f(fz[q][r]); v1 += hi_f(fz[q][r]); }
-                uint32_t t3[NU];
-                split2<NU>(v0 * gb.upd[t], v1 * gb.upd[t + 1], t3);
-#pragma unroll
-                for (int q = 0; q < NU; ++q) wz[q][r] = t3[q];
-            }
-#pragma unroll
-            for (int n = 0; n < DC / 16; ++n) {
-                uint32_t fy[NI][4];
-#pragma unroll
-                for (int q = 0; q < NI; ++q)
-                    ldsm4t(fy[q], smem_addr(sY + q * S::XY +
-                                            (kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * LC +
-                                            n * 16 + (lane >> 4) * 8));
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t b[NI][2];
-#pragma unroll
-                    for (int q = 0; q < NI; ++q) { b[q][0] = fy[q][2 * e]; b[q][1] = fy[q][2 * e + 1]; }
-                    mma_terms<NU, NI>(M[2 * n + e], wz, b);
+                    mma_terms<NP, NI>(acc[m][0], low[m][0], fp, b[0]);
+                    mma_terms<NP, NI>(acc[m][1], low[m][1], fp, b[1]);
                 }
             }
         }
@@ -429,7 +401,8 @@ la_run_kernel(const LaArgs a) {
                         const size_t at = ((size_t)(tok + row) * H + h) * DO + r0 + gc;
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            const float v0 = acc[m][n][2 * e2], v1 = acc[m][n][2 * e2 + 1];
+                            const float v0 = acc[m][n][2 * e2] + low[m][n][2 * e2];
+                            const float v1 = acc[m][n][2 * e2 + 1] + low[m][n][2 * e2 + 1];
                             if (sizeof(T) == 4 || R.out_f32)
                                 *reinterpret_cast<float2*>(static_cast<float*>(R.out) + at + 8 * n) =
                                     make_float2(v0, v1);
@@ -472,6 +445,51 @@ la_run_kernel(const LaArgs a) {
                                                       u.index * (a.sp.L / C) + c) * H + h] = sum;
                 }
             }
+        }
+        // 5. the state update: the chunk's sum on its own (fp32 accumulators from zero), then added
+        const float total = gb.total;
+        uint32_t wz[C / 16][NU][4];
+#pragma unroll
+        for (int kk = 0; kk < C / 16; ++kk) {
+            uint32_t fz[NI][4];
+#pragma unroll
+            for (int q = 0; q < NI; ++q) load_z(fz[q], sZ + q * S::Z, kk);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = kk * 16 + gc + (r >> 1) * 8;
+                float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+                for (int q = NI - 1; q >= 0; --q) { v0 += lo_f(fz[q][r]); v1 += hi_f(fz[q][r]); }
+                uint32_t t3[NU];
+                split2<NU>(v0 * gb.upd[t], v1 * gb.upd[t + 1], t3);
+#pragma unroll
+                for (int q = 0; q < NU; ++q) wz[kk][q][r] = t3[q];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < DC / 16; ++n) {
+            float sum[2][4] = {}, less[2][4] = {};
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk) {
+                uint32_t fy[NI][4];
+#pragma unroll
+                for (int q = 0; q < NI; ++q)
+                    ldsm4t(fy[q], smem_addr(sY + q * S::XY +
+                                            (kk * 16 + ((lane >> 3) & 1) * 8 + (lane & 7)) * LC +
+                                            n * 16 + (lane >> 4) * 8));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t b[NI][2];
+#pragma unroll
+                    for (int q = 0; q < NI; ++q) { b[q][0] = fy[q][2 * e]; b[q][1] = fy[q][2 * e + 1]; }
+                    mma_terms<NU, NI>(sum[e], less[e], wz[kk], b);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    M[2 * n + e][k] = fmaf(M[2 * n + e][k], total, sum[e][k] + less[e][k]);
         }
         if (warp == 0 && i + 1 < nch) chunk_gates(&gates[(i + 1) & 1], g0, g1, rev, R.u_scale);
     }
