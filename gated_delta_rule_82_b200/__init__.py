@@ -9,6 +9,7 @@ Build the library with ``python -m gated_delta_rule_82_b200.build``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -460,27 +461,52 @@ def bwd_chunked(q, k, v, alpha, beta, h0, dout, dhT=None, *, l2norm=True, rope_t
     return g
 
 
-class _on:
-    """The current device for a call whose tensors are on `device`."""
+# The calls below are used token by token and layer by layer, where the marshalling costs as much as
+# a small kernel: pointers go to ctypes as plain integers, and checks that pass are made inline.
 
-    def __init__(self, device):
-        self.device = device
+def _need(t, name, dtype, shape, device):
+    """t is a contiguous CUDA tensor of this type and shape on this device."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device \
+            and t.is_contiguous():
+        return
+    _check(t, name, dtype=dtype, shape=shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
 
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
 
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+# (the handle alone: building a Stream object costs as much as the launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, device, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _raw_stream(device.index))
+    with torch.cuda.device(device):
+        return fn(*args, _raw_stream(device.index))
+
+
+@functools.lru_cache(maxsize=256)
+def _linattn_flags(scale, qk_heads):
+    return _flags(False, 0.0, 0, scale, qk_heads=qk_heads)
+
+
+@functools.lru_cache(maxsize=256)
+def _linattn_rows_bytes(backward, B, T, H, Hk, dk, dv):
+    """Workspace bytes for B rows of T tokens (a function of the sizes alone)."""
+    return (linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv) if backward
+            else linattn_fwd_workspace_bytes(B, T, H, dk, dv))
 
 
 def _linattn_shapes(q, k, v, log_decay, cu_seqlens, cu_seqlens_cpu):
     """(B, T, n, lead, H, Hk, dk, dv, per_token, host offsets) of the chunked calls' arguments."""
     _check(q, "q")
     dev = q.device
-    _check(v, "v", dtype=q.dtype)
     packed = cu_seqlens is not None
     if not packed and q.dim() != 4:
         raise ValueError(f"q: expected [B, T, Hk, dk], got {tuple(q.shape)}")
@@ -488,35 +514,25 @@ def _linattn_shapes(q, k, v, log_decay, cu_seqlens, cu_seqlens_cpu):
         raise ValueError(f"q: expected [T, Hk, dk] or [1, T, Hk, dk], got {tuple(q.shape)}")
     if packed and q.dim() == 4 and q.shape[0] != 1:
         raise ValueError("packed sequences take a batch axis of 1 (or none)")
-    lead = tuple(q.shape[:-2])
-    if v.dim() != q.dim() or tuple(v.shape[:-2]) != lead:
-        raise ValueError(f"v: expected {lead + ('H', 'dv')}, got {tuple(v.shape)}")
-    Hk, dk = q.shape[-2:]
+    *lead, Hk, dk = q.shape
+    lead = tuple(lead)
+    if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+        raise ValueError(f"v: expected {lead + ('H', 'dv')}")
     H, dv = v.shape[-2:]
     if Hk < 1 or H < 1 or H % Hk:
         raise ValueError(f"v has {H} heads, not a multiple of q's {Hk}")
-    _check(k, "k", dtype=q.dtype, shape=q.shape)
-    per_token = log_decay.dim() != 1
-    _check(log_decay, "log_decay", dtype=torch.float32, shape=lead + (H,) if per_token else (H,))
-    host = None
-    if packed:
-        host = _host_offsets(cu_seqlens, cu_seqlens_cpu)
-        if int(host[-1]) != lead[-1]:
-            raise ValueError(f"cu_seqlens ends at {int(host[-1])}, but the token axis holds {lead[-1]}")
-        B, T, n = 1, lead[-1], host.numel() - 1
-    else:
-        B, T = lead
-        n = B
-    for t, name in ((k, "k"), (v, "v"), (log_decay, "log_decay"), (cu_seqlens, "cu_seqlens")):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, q on {dev}")
-    return B, T, n, lead, H, Hk, dk, dv, per_token, host
-
-
-def _on_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+    _need(v, "v", q.dtype, lead + (H, dv), dev)
+    _need(k, "k", q.dtype, q.shape, dev)
+    per_token = isinstance(log_decay, torch.Tensor) and log_decay.dim() != 1
+    _need(log_decay, "log_decay", torch.float32, lead + (H,) if per_token else (H,), dev)
+    if not packed:
+        return *lead, lead[0], lead, H, Hk, dk, dv, per_token, None
+    host = _host_offsets(cu_seqlens, cu_seqlens_cpu)
+    if cu_seqlens.device != dev:
+        raise ValueError(f"cu_seqlens is on {cu_seqlens.device}, q on {dev}")
+    if int(host[-1]) != lead[-1]:
+        raise ValueError(f"cu_seqlens ends at {int(host[-1])}, but the token axis holds {lead[-1]}")
+    return 1, lead[-1], host.numel() - 1, lead, H, Hk, dk, dv, per_token, host
 
 
 def linattn_fwd_workspace_bytes(B, T, H, dk, dv, cu_seqlens_cpu=None) -> int:
@@ -544,29 +560,30 @@ def linattn_fwd_chunked(q, k, v, log_decay, h0=None, *, cu_seqlens=None, cu_seql
     """
     B, T, n, lead, H, Hk, dk, dv, per_token, host = _linattn_shapes(q, k, v, log_decay, cu_seqlens,
                                                                     cu_seqlens_cpu)
-    dev = q.device
+    dev, shape, states = q.device, lead + (H, dv), (n, H, dk, dv)
     if h0 is not None:
-        _check(h0, "h0", dtype=torch.float32, shape=(n, H, dk, dv))
+        _need(h0, "h0", torch.float32, states, dev)
     if out is None:
-        out = torch.empty(lead + (H, dv), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
     else:
-        _check(out, "out", dtype=q.dtype, shape=lead + (H, dv))
+        _need(out, "out", q.dtype, shape, dev)
     if hT is not None:
-        _check(hT, "hT", dtype=torch.float32, shape=(n, H, dk, dv))
+        _need(hT, "hT", torch.float32, states, dev)
     elif want_state:
-        hT = torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev)
+        hT = torch.empty(states, dtype=torch.float32, device=dev)
     if workspace is None:   # (a workspace given is checked against the need by the library)
-        need = linattn_fwd_workspace_bytes(B, T, H, dk, dv, host)
+        need = (_linattn_rows_bytes(False, B, T, H, Hk, dk, dv) if host is None
+                else linattn_fwd_workspace_bytes(B, T, H, dk, dv, host))
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _on_device(dev, h0=h0, out=out, hT=hT, workspace=workspace)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, q on {dev}")
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(dev):
-        st = _load().ckda_linattn_fwd_chunked(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), _ptr(h0), _ptr(out),
-            _ptr(hT), B, T, _ptr(cu_seqlens), _ptr(host), n if host is not None else 0, H, dk, dv,
-            _flags(False, 0.0, 0, scale, qk_heads=Hk if Hk != H else 0), _dtype_code(q),
-            _ptr(workspace), wbytes, _stream(dev))
+    st = _call(_load().ckda_linattn_fwd_chunked, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+               log_decay.data_ptr(), int(per_token), _p(h0), out.data_ptr(), _p(hT), B, T,
+               _p(cu_seqlens), _p(host), 0 if host is None else n, H, dk, dv,
+               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q), _p(workspace),
+               wbytes)
     _raise("ckda_linattn_fwd_chunked", st)
     return out, hT
 
@@ -593,27 +610,27 @@ def linattn_bwd_chunked(q, k, v, log_decay, h0, dout, dhT=None, *, cu_seqlens=No
     """
     B, T, n, lead, H, Hk, dk, dv, per_token, host = _linattn_shapes(q, k, v, log_decay, cu_seqlens,
                                                                     cu_seqlens_cpu)
-    dev = q.device
-    _check(dout, "dout", dtype=q.dtype, shape=lead + (H, dv))
+    dev, states = q.device, (n, H, dk, dv)
+    _need(dout, "dout", q.dtype, lead + (H, dv), dev)
     if h0 is not None:
-        _check(h0, "h0", dtype=torch.float32, shape=(n, H, dk, dv))
+        _need(h0, "h0", torch.float32, states, dev)
     if dhT is not None:
-        _check(dhT, "dhT", dtype=torch.float32, shape=(n, H, dk, dv))
+        _need(dhT, "dhT", torch.float32, states, dev)
     g = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
          "dlog_decay": torch.empty_like(log_decay) if want_dlog_decay else None,
-         "dh0": torch.empty((n, H, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None}
+         "dh0": torch.empty(states, dtype=torch.float32, device=dev) if want_dh0 else None}
     if workspace is None:
-        workspace = torch.empty(linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv, host),
-                                dtype=torch.uint8, device=dev)
-    _on_device(dev, h0=h0, dout=dout, dhT=dhT, workspace=workspace)
-    wbytes = workspace.numel() * workspace.element_size()
-    with _on(dev):
-        st = _load().ckda_linattn_bwd_chunked(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), _ptr(h0), _ptr(dout),
-            _ptr(dhT), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dlog_decay"]),
-            _ptr(g["dh0"]), B, T, _ptr(cu_seqlens), _ptr(host), n if host is not None else 0, H, dk,
-            dv, _flags(False, 0.0, 0, scale, qk_heads=Hk if Hk != H else 0), _dtype_code(q),
-            _ptr(workspace), wbytes, _stream(dev))
+        need = (_linattn_rows_bytes(True, B, T, H, Hk, dk, dv) if host is None
+                else linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv, host))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, q on {dev}")
+    st = _call(_load().ckda_linattn_bwd_chunked, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+               log_decay.data_ptr(), int(per_token), _p(h0), dout.data_ptr(), _p(dhT),
+               g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), _p(g["dlog_decay"]),
+               _p(g["dh0"]), B, T, _p(cu_seqlens), _p(host), 0 if host is None else n, H, dk, dv,
+               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q),
+               workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _raise("ckda_linattn_bwd_chunked", st)
     return g
 
@@ -626,32 +643,34 @@ def linattn_decode_step(q, k, v, log_decay, state, *, scale=0.0, out=None):
     if q.dim() != 3:
         raise ValueError(f"q: expected [N, Hk, dk], got {tuple(q.shape)}")
     N, Hk, dk = q.shape
-    _check(v, "v", dtype=q.dtype)
-    if v.dim() != 3 or v.shape[0] != N:
-        raise ValueError(f"v: expected [N={N}, H, dv], got {tuple(v.shape)}")
-    H, dv = v.shape[1], v.shape[2]
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError(f"v: expected [N={N}, H, dv]")
+    H, dv = v.shape[1:]
     if Hk < 1 or H % Hk:
         raise ValueError(f"v has {H} heads, not a multiple of q's {Hk}")
     dev = q.device
-    _check(k, "k", dtype=q.dtype, shape=q.shape)
-    per_token = log_decay.dim() != 1
-    _check(log_decay, "log_decay", dtype=torch.float32, shape=(N, H) if per_token else (H,))
-    _check(state, "state", dtype=torch.float32, shape=(N, H, dk, dv))
+    _need(k, "k", q.dtype, q.shape, dev)
+    _need(v, "v", q.dtype, (N, H, dv), dev)
+    per_token = isinstance(log_decay, torch.Tensor) and log_decay.dim() != 1
+    _need(log_decay, "log_decay", torch.float32, (N, H) if per_token else (H,), dev)
+    _need(state, "state", torch.float32, (N, H, dk, dv), dev)
     if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=dev)
+        out = torch.empty_like(v)
     else:
-        _check(out, "out", dtype=q.dtype, shape=(N, H, dv))
-    _on_device(dev, k=k, v=v, log_decay=log_decay, state=state, out=out)
-    with _on(dev):
-        st = _load().ckda_linattn_decode_step(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), int(per_token), _ptr(state), _ptr(out), N,
-            H, dk, dv, _flags(False, 0.0, 0, scale, qk_heads=Hk if Hk != H else 0), _dtype_code(q),
-            _stream(dev))
+        _need(out, "out", q.dtype, v.shape, dev)
+    st = _call(_load().ckda_linattn_decode_step, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+               log_decay.data_ptr(), int(per_token), state.data_ptr(), out.data_ptr(), N, H, dk, dv,
+               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q))
     _raise("ckda_linattn_decode_step", st)
     return out
 
 
 GATE_ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_flags(post_group, gate_act, res_scale, eps):
+    return _NormFlags(post_group, GATE_ACTS[gate_act], res_scale, eps)
 
 
 def _norm_args(y, gate, gate_act, residual, post_group, post_weight, res_scale, res_vector, eps,
@@ -660,23 +679,22 @@ def _norm_args(y, gate, gate_act, residual, post_group, post_weight, res_scale, 
     _check(y, "y")
     if y.dim() < 1 or y.numel() == 0:
         raise ValueError(f"y: expected [.., D] with at least one row, got {tuple(y.shape)}")
-    D = y.shape[-1]
-    for t, name in ((gate, "gate"), (residual, "residual")):
-        if t is not None:
-            _check(t, name, dtype=y.dtype, shape=y.shape)
+    D, dev = y.shape[-1], y.device
+    if gate is not None:
+        _need(gate, "gate", y.dtype, y.shape, dev)
+    if residual is not None:
+        _need(residual, "residual", y.dtype, y.shape, dev)
     if (gate is None) != (gate_act == "none"):
         raise ValueError("gate and gate_act go together (gate_act 'none' without a gate)")
     if post_weight is not None:
         if not post_group:
             raise ValueError("post_weight without a first norm (post_group = 0)")
-        _check(post_weight, "post_weight", dtype=torch.float32, shape=(post_group,))
-    for t, name in ((res_vector, "res_vector"), (pre_weight, "pre_weight")):
-        if t is not None:
-            _check(t, name, dtype=torch.float32, shape=(D,))
-    _on_device(y.device, gate=gate, residual=residual, post_weight=post_weight,
-               res_vector=res_vector, pre_weight=pre_weight)
-    return y.numel() // D, D, _NormFlags(int(post_group), GATE_ACTS[gate_act], float(res_scale),
-                                         float(eps))
+        _need(post_weight, "post_weight", torch.float32, (post_group,), dev)
+    if res_vector is not None:
+        _need(res_vector, "res_vector", torch.float32, (D,), dev)
+    if pre_weight is not None:
+        _need(pre_weight, "pre_weight", torch.float32, (D,), dev)
+    return y.numel() // D, D, _norm_flags(int(post_group), gate_act, float(res_scale), float(eps))
 
 
 def block_norm(y, *, gate=None, gate_act="none", residual=None, post_group=0, post_weight=None,
@@ -702,21 +720,20 @@ def block_norm(y, *, gate=None, gate_act="none", residual=None, post_group=0, po
     if h is None:
         h = torch.empty_like(y)
     else:
-        _check(h, "h", dtype=y.dtype, shape=y.shape)
+        _need(h, "h", y.dtype, y.shape, y.device)
     if pre_norm:
         if n is None:
             n = torch.empty_like(y)
         else:
-            _check(n, "n", dtype=y.dtype, shape=y.shape)
-    _on_device(y.device, h=h, n=n)
-    with _on(y.device):
-        st = _load().ckda_block_norm(_ptr(y), _ptr(gate), _ptr(residual), _ptr(post_weight),
-                                     _ptr(res_vector), _ptr(pre_weight), _ptr(h), _ptr(n), rows, D,
-                                     flags, _dtype_code(y), _stream(y.device))
+            _need(n, "n", y.dtype, y.shape, y.device)
+    st = _call(_load().ckda_block_norm, y.device, y.data_ptr(), _p(gate), _p(residual),
+               _p(post_weight), _p(res_vector), _p(pre_weight), h.data_ptr(), _p(n), rows, D, flags,
+               _dtype_code(y))
     _raise("ckda_block_norm", st)
     return h, n
 
 
+@functools.lru_cache(maxsize=256)
 def block_norm_bwd_workspace_bytes(rows, D, post_group=0) -> int:
     n = _load().ckda_block_norm_bwd_workspace_bytes(rows, D, post_group)
     if n == ctypes.c_size_t(-1).value:
@@ -741,10 +758,12 @@ def block_norm_bwd(y, dh, dn=None, *, gate=None, gate_act="none", residual=None,
         raise ValueError("dh and dn are both missing")
     if pre_weight is not None and not pre_norm:
         raise ValueError("pre_weight without pre_norm")
-    for t, name in ((dh, "dh"), (dn, "dn")):
-        if t is not None:
-            _check(t, name, dtype=y.dtype, shape=y.shape)
-    _on_device(y.device, dh=dh, dn=dn, workspace=workspace)
+    if dh is not None:
+        _need(dh, "dh", y.dtype, y.shape, y.device)
+    if dn is not None:
+        _need(dn, "dn", y.dtype, y.shape, y.device)
+    if workspace is not None and workspace.device != y.device:
+        raise ValueError(f"workspace is on {workspace.device}, y on {y.device}")
     like = lambda t: None if t is None else torch.empty_like(t)
     g = {"dy": torch.empty_like(y), "dgate": like(gate), "dresidual": like(residual),
          "dpost_weight": like(post_weight), "dres_vector": like(res_vector), "dpre_weight": None}
@@ -756,13 +775,11 @@ def block_norm_bwd(y, dh, dn=None, *, gate=None, gate_act="none", residual=None,
         workspace = torch.empty(block_norm_bwd_workspace_bytes(rows, D, post_group),
                                 dtype=torch.uint8, device=y.device)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(y.device):
-        st = _load().ckda_block_norm_bwd(
-            _ptr(y), _ptr(gate), _ptr(residual), _ptr(post_weight), _ptr(res_vector),
-            _ptr(pre_weight), _ptr(dh), _ptr(dn), _ptr(g["dy"]), _ptr(g["dgate"]),
-            _ptr(g["dresidual"]), _ptr(g["dpost_weight"]), _ptr(g["dres_vector"]),
-            _ptr(g["dpre_weight"]) if dn is not None else None, rows, D, flags, _dtype_code(y),
-            _ptr(workspace), wbytes, _stream(y.device))
+    st = _call(_load().ckda_block_norm_bwd, y.device, y.data_ptr(), _p(gate), _p(residual),
+               _p(post_weight), _p(res_vector), _p(pre_weight), _p(dh), _p(dn), g["dy"].data_ptr(),
+               _p(g["dgate"]), _p(g["dresidual"]), _p(g["dpost_weight"]), _p(g["dres_vector"]),
+               _p(g["dpre_weight"]) if dn is not None else None, rows, D, flags, _dtype_code(y),
+               _p(workspace), wbytes)
     _raise("ckda_block_norm_bwd", st)
     return g
 

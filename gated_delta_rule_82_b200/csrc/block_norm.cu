@@ -25,28 +25,53 @@ constexpr int E = 8;      // channels per thread
 
 enum { kActNone = 0, kActSigmoid = 1, kActSilu = 2 };
 
-// 8 consecutive channels.  kVec: the row starts on a 16-byte boundary and D is a multiple of 8.
+// 8 consecutive channels as they lie in memory, so that a row that is requested ahead costs few
+// registers.  kVec: rows start on 16-byte boundaries and D is a multiple of 8.
 template <typename T, bool kVec>
-__device__ __forceinline__ void load_e(const T* p, int left, float v[E]) {
-    if constexpr (kVec) {
-        if (left > 0) {
-            if constexpr (sizeof(T) == 2) {
-                Vec16<T, 8>::load(p, v);
-            } else {
-                Vec16<T, 4>::load(p, v);
-                Vec16<T, 4>::load(p + 4, v + 4);
-            }
-            return;
+struct Raw {
+    static constexpr int N = kVec ? 8 * (int)sizeof(T) / 16 : 1;
+    uint4 w[N];
+    T e[kVec ? 1 : E];
+
+    __device__ __forceinline__ void load(const void* base, size_t at, int left) {
+        const T* p = static_cast<const T*>(base) + at;
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[i] = left > 0 ? *reinterpret_cast<const uint4*>(p + i * (16 / (int)sizeof(T)))
+                                : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) e[i] = i < left ? p[i] : from_f32<T>(0.f);
         }
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = 0.f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = i < left ? to_f32(p[i]) : 0.f;
     }
-}
+    __device__ __forceinline__ void clear() {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) e[i] = from_f32<T>(0.f);
+        }
+    }
+    // channel i (a constant after unrolling)
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (!kVec) return to_f32(e[i]);
+        if constexpr (kVec && sizeof(T) == 4) {
+            const uint4& q = w[i >> 2];
+            return __uint_as_float((i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w);
+        }
+        if constexpr (kVec && sizeof(T) == 2) {
+            const uint4& q = w[0];
+            const uint32_t x = (i >> 1) == 0 ? q.x : (i >> 1) == 1 ? q.y : (i >> 1) == 2 ? q.z : q.w;
+            return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+        }
+        return 0.f;
+    }
+};
 template <typename T, bool kVec>
-__device__ __forceinline__ void store_e(T* p, int left, const float v[E]) {
+__device__ __forceinline__ void store_e(void* base, size_t at, int left, const float v[E]) {
+    T* p = static_cast<T*>(base) + at;
     if constexpr (kVec) {
         if (left > 0) {
             if constexpr (sizeof(T) == 2) {
@@ -100,158 +125,255 @@ __device__ __forceinline__ float2 sigmoid2(float z) {
     return z >= 0.f ? make_float2(inv, e * inv) : make_float2(e * inv, inv);
 }
 
-struct Pieces {           // of the forward, per channel
-    float yhat[E], u[E], a[E], m[E], h[E];
-    float r1;
-};
-
-// u, m, h of 8 channels from the loaded rows.
-template <int TPR>
-__device__ __forceinline__ void forward_row(const BlockNormArgs& p, int D, const float y[E],
-                                            const float z[E], const float x[E], const float wp[E],
-                                            const float s[E], RowSum<TPR>& row, Pieces& f) {
-    if (p.W) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) ss += y[i] * y[i];
-        f.r1 = rsqrtf(group_w_sum<TPR>(ss, p.W, D, row) / (float)p.W + p.eps);
-    }
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        f.yhat[i] = p.W ? y[i] * f.r1 : y[i];
-        f.u[i] = p.W ? f.yhat[i] * wp[i] : y[i];
-        f.a[i] = 1.f;
-        if (p.gate) {
-            const float g = sigmoid2(z[i]).x;
-            f.a[i] = p.act == kActSilu ? z[i] * g : g;
+// Weight vectors (fp32) in shared memory: [post][pre][s], the post weight once per row group of the
+// row, ones where a vector is missing; loaded by the whole CTA.
+struct Weights {
+    float *post, *pre, *s;
+    __device__ __forceinline__ void load(const BlockNormArgs& p, float* base) {
+        const int D = p.D;
+        post = base;
+        pre = post + (p.W ? D : 0);
+        s = pre + (p.w_pre ? D : 0);
+        for (int c = threadIdx.x; c < D; c += blockDim.x) {
+            if (p.W) post[c] = p.w_post ? __ldg(p.w_post + (p.W == D ? c : c % p.W)) : 1.f;
+            if (p.w_pre) pre[c] = __ldg(p.w_pre + c);
+            if (p.r) s[c] = __ldg(p.r + c) * p.scale;
         }
-        f.m[i] = f.u[i] * f.a[i];
-        f.h[i] = x[i] + s[i] * f.m[i];
+        __syncthreads();
+    }
+};
+size_t weights_floats(const BlockNormArgs& p) {
+    return (size_t)p.D * ((p.W != 0) + (p.w_pre != nullptr) + (p.r != nullptr));
+}
+// channel c + i of a vector in shared memory (rows of 8: two 16-byte reads)
+template <bool kVec>
+__device__ __forceinline__ void take(const float* v, int c, int left, float w[E]) {
+    if constexpr (kVec) {
+        if (left > 0) {
+            Vec16<float, 4>::load(v + c, w);
+            Vec16<float, 4>::load(v + c + 4, w + 4);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) w[i] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) w[i] = i < left ? v[c + i] : 0.f;
     }
 }
 
-// The per-channel vectors (fp32; their length need not be a multiple of 8).
-__device__ __forceinline__ void load_vec(const float* p, int c, int left, int wrap, float dflt,
-                                         float v[E]) {
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-        v[i] = p && i < left ? __ldg(p + (wrap ? (c + i) % wrap : c + i)) : dflt;
+// The gate's factor.
+__device__ __forceinline__ float gate_of(const BlockNormArgs& p, float z) {
+    const float g = sigmoid2(z).x;
+    return p.act == kActSilu ? z * g : g;
 }
+
+// The root of the first norm for this thread's group, and m (the gated value) of its 8 channels.
+template <typename T, int TPR, bool kVec>
+__device__ __forceinline__ float first_norm(const BlockNormArgs& p, const Raw<T, kVec>& y,
+                                            RowSum<TPR>& row) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) ss += y[i] * y[i];
+    return rsqrtf(group_w_sum<TPR>(ss, p.W, p.D, row) / (float)p.W + p.eps);
+}
+
+template <int TPR>
+constexpr int threads_of() { return TPR < 128 ? 128 : TPR; }
+// CTAs per SM that the register budget is set for: the kernels live on loads in flight
+template <int TPR>
+constexpr int fwd_ctas() { return 1024 / threads_of<TPR>(); }
+template <int TPR>
+constexpr int bwd_ctas() { return TPR >= 1024 ? 1 : 768 / threads_of<TPR>(); }
 
 template <typename T, int TPR, bool kVec>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(threads_of<TPR>(), fwd_ctas<TPR>())
 block_norm_kernel(const BlockNormArgs p) {
-    constexpr int THREADS = TPR < 128 ? 128 : TPR, RPC = THREADS / TPR;
+    constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
+    extern __shared__ __align__(16) float sw[];
     __shared__ float slots[2 * THREADS / 32];
     RowSum<TPR> row_sum{slots};
     const int D = p.D, sub = threadIdx.x / TPR, c = (threadIdx.x % TPR) * E, left = D - c;
-    float wp[E], wn[E], s[E];
-    load_vec(p.w_post, c, left, p.W, 1.f, wp);
-    load_vec(p.w_pre, c, left, 0, 1.f, wn);
-    load_vec(p.r, c, left, 0, 1.f, s);
-#pragma unroll
-    for (int i = 0; i < E; ++i) s[i] *= p.scale;
+    const long long step = (long long)gridDim.x * RPC;
+    long long r = (long long)blockIdx.x * RPC + sub;
+    // the first row is requested before the weights are waited for, every other one a row ahead
+    Raw<T, kVec> y, z, x;
+    auto request = [&](long long row, Raw<T, kVec>& y, Raw<T, kVec>& z, Raw<T, kVec>& x) {
+        const int l = row < p.rows ? left : 0;
+        const size_t at = (size_t)(row < p.rows ? row : 0) * D + c;
+        y.load(p.y, at, l);
+        if (p.gate) z.load(p.gate, at, l);
+        if (p.x) x.load(p.x, at, l);
+    };
+    z.clear();
+    x.clear();
+    request(r, y, z, x);
+    Weights w;
+    w.load(p, sw);
     // (every thread of a CTA goes through the same number of rows: sums synchronise)
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < p.rows; r0 += (long long)gridDim.x * RPC) {
-        const long long r = r0 + sub;
-        const bool in = r < p.rows;
-        const int l = in ? left : 0;
-        const size_t at = (size_t)(in ? r : 0) * D + c;
-        float y[E], z[E], x[E];
-        load_e<T, kVec>((const T*)p.y + at, l, y);
-        load_e<T, kVec>((const T*)p.gate + at, p.gate ? l : 0, z);
-        load_e<T, kVec>((const T*)p.x + at, p.x ? l : 0, x);
-        Pieces f;
-        forward_row<TPR>(p, D, y, z, x, wp, s, row_sum, f);
-        store_e<T, kVec>((T*)p.h + at, l, f.h);
+    for (long long r0 = (long long)blockIdx.x * RPC; r0 < p.rows; r0 += step, r += step) {
+        const int l = r < p.rows ? left : 0;
+        const size_t at = (size_t)(r < p.rows ? r : 0) * D + c;
+        Raw<T, kVec> ny, nz, nx;
+        nz.clear();
+        nx.clear();
+        if (r0 + step < p.rows) request(r + step, ny, nz, nx);
+        float h[E], v[E];
+        if (p.W) {
+            const float r1 = first_norm<T, TPR, kVec>(p, y, row_sum);
+            take<kVec>(w.post, c, left, v);
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[i] = y[i] * r1 * v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[i] = y[i];
+        }
+        if (p.gate) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[i] *= gate_of(p, z[i]);
+        }
+        if (p.r) {
+            take<kVec>(w.s, c, left, v);
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[i] = x[i] + v[i] * h[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) h[i] = x[i] + p.scale * h[i];
+        }
+        store_e<T, kVec>(p.h, at, l, h);
         if (p.n) {
             float ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) ss += i < left ? f.h[i] * f.h[i] : 0.f;
+            for (int i = 0; i < E; ++i) ss += h[i] * h[i];
             const float r2 = rsqrtf(row_sum(ss) / (float)D + p.eps);
-            float n[E];
+            if (p.w_pre) {
+                take<kVec>(w.pre, c, left, v);
 #pragma unroll
-            for (int i = 0; i < E; ++i) n[i] = f.h[i] * r2 * wn[i];
-            store_e<T, kVec>((T*)p.n + at, l, n);
+                for (int i = 0; i < E; ++i) h[i] *= r2 * v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) h[i] *= r2;
+            }
+            store_e<T, kVec>(p.n, at, l, h);
         }
+        y = ny;
+        z = nz;
+        x = nx;
     }
 }
 
 template <typename T, int TPR, bool kVec>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(threads_of<TPR>(), bwd_ctas<TPR>())
 block_norm_bwd_kernel(const BlockNormArgs p, const BlockNormGrads g) {
-    constexpr int THREADS = TPR < 128 ? 128 : TPR, RPC = THREADS / TPR;
+    constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
+    extern __shared__ __align__(16) float sw[];
     __shared__ float slots[2 * THREADS / 32];
     RowSum<TPR> row_sum{slots};
     const int D = p.D, sub = threadIdx.x / TPR, c = (threadIdx.x % TPR) * E, left = D - c;
-    float wp[E], wn[E], s[E], dwp[E], dwn[E], dr[E];
-    load_vec(p.w_post, c, left, p.W, 1.f, wp);
-    load_vec(p.w_pre, c, left, 0, 1.f, wn);
-    load_vec(p.r, c, left, 0, 1.f, s);
+    float dwp[E], dwn[E], dr[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        s[i] *= p.scale;
-        dwp[i] = dwn[i] = dr[i] = 0.f;
-    }
+    for (int i = 0; i < E; ++i) dwp[i] = dwn[i] = dr[i] = 0.f;
+    Weights w;
+    w.load(p, sw);
     for (long long r0 = (long long)blockIdx.x * RPC; r0 < p.rows; r0 += (long long)gridDim.x * RPC) {
         const long long r = r0 + sub;
-        const bool in = r < p.rows;
-        const int l = in ? left : 0;
-        const size_t at = (size_t)(in ? r : 0) * D + c;
-        float y[E], z[E], x[E], dh[E], dn[E];
-        load_e<T, kVec>((const T*)p.y + at, l, y);
-        load_e<T, kVec>((const T*)p.gate + at, p.gate ? l : 0, z);
-        load_e<T, kVec>((const T*)p.x + at, p.x && g.dn ? l : 0, x);
-        load_e<T, kVec>((const T*)g.dh + at, g.dh ? l : 0, dh);
-        load_e<T, kVec>((const T*)g.dn + at, g.dn ? l : 0, dn);
-        Pieces f;
-        forward_row<TPR>(p, D, y, z, x, wp, s, row_sum, f);
+        const int l = r < p.rows ? left : 0;
+        const size_t at = (size_t)(r < p.rows ? r : 0) * D + c;
+        Raw<T, kVec> y, z, x, rh, rn;
+        z.clear();
+        x.clear();
+        rh.clear();
+        y.load(p.y, at, l);
+        if (p.gate) z.load(p.gate, at, l);
         if (g.dn) {
-            float ss = 0.f, dd = 0.f;
+            rn.load(g.dn, at, l);
+            if (p.x) x.load(p.x, at, l);
+        }
+        if (g.dh) rh.load(g.dh, at, l);
+        // the forward's values (in registers: u, and the gate's factor where it is used)
+        float r1 = 1.f, u[E], v[E], dh[E];
+        if (p.W) {
+            r1 = first_norm<T, TPR, kVec>(p, y, row_sum);
+            take<kVec>(w.post, c, left, v);
+#pragma unroll
+            for (int i = 0; i < E; ++i) u[i] = y[i] * r1 * v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) u[i] = y[i];
+        }
+        float s[E];
+        if (p.r) {
+            take<kVec>(w.s, c, left, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) s[i] = p.scale;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) dh[i] = rh[i];
+        if (g.dn) {
+            float ss = 0.f, dd = 0.f, h[E];
+            if (p.w_pre) {
+                take<kVec>(w.pre, c, left, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[i] = 1.f;
+            }
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                ss += i < left ? f.h[i] * f.h[i] : 0.f;
-                dd += dn[i] * wn[i] * f.h[i];
+                h[i] = x[i] + s[i] * u[i] * (p.gate ? gate_of(p, z[i]) : 1.f);
+                ss += h[i] * h[i];
+                dd += rn[i] * v[i] * h[i];
             }
             const float r2 = rsqrtf(row_sum(ss) / (float)D + p.eps);
             const float mean = row_sum(dd) * r2 / (float)D;       // mean of dn w hhat
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float hhat = f.h[i] * r2;
-                dh[i] += r2 * (dn[i] * wn[i] - hhat * mean);
-                dwn[i] += dn[i] * hhat;
+                const float hhat = h[i] * r2;
+                dh[i] += r2 * (rn[i] * v[i] - hhat * mean);
+                dwn[i] += rn[i] * hhat;
             }
         }
-        if (g.dx) store_e<T, kVec>((T*)g.dx + at, l, dh);
-        float du[E], dz[E];
+        if (g.dx) store_e<T, kVec>(g.dx, at, l, dh);
+        // dh becomes the gradient of u; the gate's gradient goes out on the way
+        if (p.gate) {
+            float dz[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (l > 0) dr[i] += dh[i] * f.m[i];
-            const float dm = dh[i] * s[i];
-            du[i] = dm * f.a[i];
-            dz[i] = 0.f;
-            if (p.gate) {
+            for (int i = 0; i < E; ++i) {
                 const float2 sg = sigmoid2(z[i]);
-                const float slope = p.act == kActSilu ? sg.x * (1.f + z[i] * sg.y) : sg.x * sg.y;
-                dz[i] = dm * f.u[i] * slope;
+                const bool silu = p.act == kActSilu;
+                const float f = silu ? z[i] * sg.x : sg.x;
+                const float slope = silu ? sg.x * (1.f + z[i] * sg.y) : sg.x * sg.y;
+                dr[i] += dh[i] * u[i] * f;
+                const float dm = dh[i] * s[i];
+                dz[i] = dm * u[i] * slope;
+                dh[i] = dm * f;
+            }
+            store_e<T, kVec>(g.dgate, at, l, dz);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                dr[i] += dh[i] * u[i];
+                dh[i] *= s[i];
             }
         }
-        if (p.gate) store_e<T, kVec>((T*)g.dgate + at, l, dz);
         if (p.W) {
             float dd = 0.f;
+            take<kVec>(w.post, c, left, v);
 #pragma unroll
-            for (int i = 0; i < E; ++i) dd += du[i] * wp[i] * f.yhat[i];
+            for (int i = 0; i < E; ++i) dd += dh[i] * v[i] * (y[i] * r1);
             const float mean = group_w_sum<TPR>(dd, p.W, D, row_sum) / (float)p.W;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                dwp[i] += du[i] * f.yhat[i];
-                du[i] = f.r1 * (du[i] * wp[i] - f.yhat[i] * mean);
+                const float yhat = y[i] * r1;
+                dwp[i] += dh[i] * yhat;
+                dh[i] = r1 * (dh[i] * v[i] - yhat * mean);
             }
         }
-        store_e<T, kVec>((T*)g.dy + at, l, du);
+        store_e<T, kVec>(g.dy, at, l, dh);
     }
     // this CTA's sums: [CTA][W], [CTA][D], [CTA][D] for the weights that want one
-    __shared__ float fold[THREADS * E];
+    __syncthreads();
+    float* fold = sw;         // (the weights are done with; the launch leaves room for both)
     float* to = g.partial;
     auto put = [&](const float v[E], int width) {
         __syncthreads();
@@ -288,8 +410,16 @@ block_norm_reduce_kernel(const ReduceArgs a) {
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
     if (blockIdx.x * 32 >= cols) return;
     float s = 0.f;
-    if (c < cols)
-        for (int r = ty; r < a.rows; r += 32) s += a.src[k][(size_t)r * cols + c];
+    if (c < cols) {
+        const float* p = a.src[k] + c;
+        int r = ty;
+        for (; r + 96 < a.rows; r += 128) {       // four rows in flight
+            const float a0 = p[(size_t)r * cols], a1 = p[(size_t)(r + 32) * cols];
+            const float a2 = p[(size_t)(r + 64) * cols], a3 = p[(size_t)(r + 96) * cols];
+            s += (a0 + a1) + (a2 + a3);
+        }
+        for (; r < a.rows; r += 32) s += p[(size_t)r * cols];
+    }
     part[ty][tx] = s;
     __syncthreads();
     s = warp_sum(part[tx][ty]);
@@ -308,39 +438,69 @@ int rows_per_cta(int D) {
     return t < 128 ? 128 / t : 1;
 }
 
-template <typename T, bool kVec>
-cudaError_t launch_fwd(const BlockNormArgs& p, int grid, cudaStream_t s) {
-    switch (threads_per_row(p.D)) {
-        case 32: block_norm_kernel<T, 32, kVec><<<grid, 128, 0, s>>>(p); break;
-        case 64: block_norm_kernel<T, 64, kVec><<<grid, 128, 0, s>>>(p); break;
-        case 128: block_norm_kernel<T, 128, kVec><<<grid, 128, 0, s>>>(p); break;
-        case 256: block_norm_kernel<T, 256, kVec><<<grid, 256, 0, s>>>(p); break;
-        case 512: block_norm_kernel<T, 512, kVec><<<grid, 512, 0, s>>>(p); break;
-        default: block_norm_kernel<T, 1024, kVec><<<grid, 1024, 0, s>>>(p); break;
-    }
+// Dynamic shared memory above the default needs the attribute, per kernel and device.
+template <typename K>
+cudaError_t room(K kern, size_t bytes) {
+    return bytes > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    (int)bytes)
+                             : cudaSuccess;
+}
+
+template <typename T, int TPR, bool kVec>
+cudaError_t fwd_t(const BlockNormArgs& p, cudaStream_t s) {
+    constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
+    const long long ctas = (p.rows + RPC - 1) / RPC, most = 148ll * fwd_ctas<TPR>();
+    const size_t smem = weights_floats(p) * sizeof(float);
+    auto kern = block_norm_kernel<T, TPR, kVec>;
+    const cudaError_t e = room(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(int)(ctas < most ? ctas : most), THREADS, smem, s>>>(p);
     return cudaGetLastError();
+}
+
+template <typename T, int TPR, bool kVec>
+cudaError_t bwd_t(const BlockNormArgs& p, const BlockNormGrads& g, int grid, cudaStream_t s) {
+    constexpr int THREADS = threads_of<TPR>();
+    const size_t wb = weights_floats(p) * sizeof(float), fb = (size_t)THREADS * E * sizeof(float);
+    const size_t smem = wb > fb ? wb : fb;
+    auto kern = block_norm_bwd_kernel<T, TPR, kVec>;
+    const cudaError_t e = room(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, THREADS, smem, s>>>(p, g);
+    return cudaGetLastError();
+}
+
+template <typename T, bool kVec>
+cudaError_t launch_fwd(const BlockNormArgs& p, cudaStream_t s) {
+    switch (threads_per_row(p.D)) {
+        case 32: return fwd_t<T, 32, kVec>(p, s);
+        case 64: return fwd_t<T, 64, kVec>(p, s);
+        case 128: return fwd_t<T, 128, kVec>(p, s);
+        case 256: return fwd_t<T, 256, kVec>(p, s);
+        case 512: return fwd_t<T, 512, kVec>(p, s);
+        default: return fwd_t<T, 1024, kVec>(p, s);
+    }
 }
 
 template <typename T, bool kVec>
 cudaError_t launch_bwd(const BlockNormArgs& p, const BlockNormGrads& g, int grid, cudaStream_t s) {
     switch (threads_per_row(p.D)) {
-        case 32: block_norm_bwd_kernel<T, 32, kVec><<<grid, 128, 0, s>>>(p, g); break;
-        case 64: block_norm_bwd_kernel<T, 64, kVec><<<grid, 128, 0, s>>>(p, g); break;
-        case 128: block_norm_bwd_kernel<T, 128, kVec><<<grid, 128, 0, s>>>(p, g); break;
-        case 256: block_norm_bwd_kernel<T, 256, kVec><<<grid, 256, 0, s>>>(p, g); break;
-        case 512: block_norm_bwd_kernel<T, 512, kVec><<<grid, 512, 0, s>>>(p, g); break;
-        default: block_norm_bwd_kernel<T, 1024, kVec><<<grid, 1024, 0, s>>>(p, g); break;
+        case 32: return bwd_t<T, 32, kVec>(p, g, grid, s);
+        case 64: return bwd_t<T, 64, kVec>(p, g, grid, s);
+        case 128: return bwd_t<T, 128, kVec>(p, g, grid, s);
+        case 256: return bwd_t<T, 256, kVec>(p, g, grid, s);
+        case 512: return bwd_t<T, 512, kVec>(p, g, grid, s);
+        default: return bwd_t<T, 1024, kVec>(p, g, grid, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace
 
 // CTAs of the backward: each keeps the weight gradients of the rows it takes, so there are only
-// as many as run side by side (2048 threads per SM at most, and half that by registers).
+// as many as run side by side.
 int block_norm_bwd_grid(long long rows, int D) {
     const int threads = threads_per_row(D) < 128 ? 128 : threads_per_row(D);
-    const long long most = 148ll * (threads >= 1024 ? 1 : 1024 / threads);
+    const long long most = 148ll * (threads >= 1024 ? 1 : 768 / threads);
     const long long need = (rows + rows_per_cta(D) - 1) / rows_per_cta(D);
     return (int)(need < most ? need : most);
 }
@@ -350,15 +510,10 @@ size_t block_norm_bwd_partial_floats(long long rows, int D, int W) {
 }
 
 cudaError_t launch_block_norm(const BlockNormArgs& p, ckda_dtype dtype, cudaStream_t s) {
-    const long long ctas = (p.rows + rows_per_cta(p.D) - 1) / rows_per_cta(p.D);
-    const int threads = threads_per_row(p.D) < 128 ? 128 : threads_per_row(p.D);
-    const long long most = 148ll * 2048 / threads;   // (as many as run side by side)
-    const int grid = (int)(ctas < most ? ctas : most);
     const bool vec = p.D % E == 0;
     if (dtype == CKDA_BF16)
-        return vec ? launch_fwd<__nv_bfloat16, true>(p, grid, s)
-                   : launch_fwd<__nv_bfloat16, false>(p, grid, s);
-    return vec ? launch_fwd<float, true>(p, grid, s) : launch_fwd<float, false>(p, grid, s);
+        return vec ? launch_fwd<__nv_bfloat16, true>(p, s) : launch_fwd<__nv_bfloat16, false>(p, s);
+    return vec ? launch_fwd<float, true>(p, s) : launch_fwd<float, false>(p, s);
 }
 
 cudaError_t launch_block_norm_bwd(const BlockNormArgs& p, const BlockNormGrads& g,
