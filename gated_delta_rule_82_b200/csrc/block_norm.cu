@@ -88,18 +88,40 @@ __device__ __forceinline__ void store_e(void* base, size_t at, int left, const f
     }
 }
 
-// Sums over the threads of one row.  TPR threads hold a row; rows of up to 32 threads stay in a
-// warp, longer ones meet in shared memory (one slot per warp, two buffers in turn).
+// Sums over the threads of one row, one or two values at a time.  TPR threads hold a row; rows of up
+// to 32 threads stay in a warp, longer ones meet in shared memory (one slot per warp, two buffers in
+// turn).
 template <int TPR>
 struct RowSum {
-    float* slots;     // [2][warps of the CTA]
+    float2* slots;    // [2][warps of the CTA]
     int turn = 0;
+    __device__ __forceinline__ float2 both(float2 x) {
+        x.x = group_sum<TPR < 32 ? TPR : 32>(x.x);
+        x.y = group_sum<TPR < 32 ? TPR : 32>(x.y);
+        if constexpr (TPR > 32) {
+            constexpr int WPR = TPR / 32;
+            const int warp = threadIdx.x >> 5;
+            float2* s = slots + turn * (blockDim.x >> 5);
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0) s[warp] = x;
+            __syncthreads();
+            const int w0 = warp / WPR * WPR;
+            x = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                const float2 y = s[w0 + w];
+                x.x += y.x;
+                x.y += y.y;
+            }
+        }
+        return x;
+    }
     __device__ __forceinline__ float operator()(float x) {
         x = group_sum<TPR < 32 ? TPR : 32>(x);
         if constexpr (TPR > 32) {
             constexpr int WPR = TPR / 32;
             const int warp = threadIdx.x >> 5;
-            float* s = slots + turn * (blockDim.x >> 5);
+            float* s = reinterpret_cast<float*>(slots + turn * (blockDim.x >> 5));
             turn ^= 1;
             if ((threadIdx.x & 31) == 0) s[warp] = x;
             __syncthreads();
@@ -119,9 +141,36 @@ __device__ __forceinline__ float group_w_sum(float x, int W, int D, RowSum<TPR>&
     return x;
 }
 
+// 2^x and 1 / x of the special function unit (about 2^-22 relative): with the exact forms the gate
+// took 40 of 67 instructions per channel, and the kernel was bound by them, not by memory.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// exp(-z).  For fp32 results the product z log2(e) is kept in two parts: its rounding, |z| 2^-24,
+// would be the largest error.
+template <typename T>
+__device__ __forceinline__ float exp_neg(float z) {
+    const float kL = -1.44269504f;
+    const float h = z * kL;
+    if constexpr (sizeof(T) == 2) return ex2(h);
+    // (-inf and overflow: nothing to correct)
+    const float l = fmaf(z, kL, -h), e = ex2(h);
+    return fabsf(h) < 120.f ? fmaf(e, l * 0.693147181f, e) : e;
+}
+// logistic(z)
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + exp_neg<T>(z)); }
 // logistic(z) and 1 - logistic(z), neither by cancellation
+template <typename T>
 __device__ __forceinline__ float2 sigmoid2(float z) {
-    const float e = expf(-fabsf(z)), inv = 1.f / (1.f + e);
+    const float e = exp_neg<T>(fabsf(z)), inv = rcp(1.f + e);
     return z >= 0.f ? make_float2(inv, e * inv) : make_float2(e * inv, inv);
 }
 
@@ -135,7 +184,7 @@ struct Weights {
         pre = post + (p.W ? D : 0);
         s = pre + (p.w_pre ? D : 0);
         for (int c = threadIdx.x; c < D; c += blockDim.x) {
-            if (p.W) post[c] = p.w_post ? __ldg(p.w_post + (p.W == D ? c : c % p.W)) : 1.f;
+            if (p.W) post[c] = p.w_post ? __ldg(p.w_post + (p.W == D ? c : c & (p.W - 1))) : 1.f;
             if (p.w_pre) pre[c] = __ldg(p.w_pre + c);
             if (p.r) s[c] = __ldg(p.r + c) * p.scale;
         }
@@ -163,19 +212,20 @@ __device__ __forceinline__ void take(const float* v, int c, int left, float w[E]
 }
 
 // The gate's factor.
-__device__ __forceinline__ float gate_of(const BlockNormArgs& p, float z) {
-    const float g = sigmoid2(z).x;
-    return p.act == kActSilu ? z * g : g;
+template <typename T, int kAct>
+__device__ __forceinline__ float gate_of(float z) {
+    const float g = sigmoid<T>(z);
+    return kAct == kActSilu ? z * g : g;
 }
 
 // The root of the first norm for this thread's group, and m (the gated value) of its 8 channels.
 template <typename T, int TPR, bool kVec>
-__device__ __forceinline__ float first_norm(const BlockNormArgs& p, const Raw<T, kVec>& y,
+__device__ __forceinline__ float first_norm(const BlockNormArgs& p, const Raw<T, kVec>& y, float inv_w,
                                             RowSum<TPR>& row) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) ss += y[i] * y[i];
-    return rsqrtf(group_w_sum<TPR>(ss, p.W, p.D, row) / (float)p.W + p.eps);
+    return rsqrtf(group_w_sum<TPR>(ss, p.W, p.D, row) * inv_w + p.eps);
 }
 
 template <int TPR>
@@ -184,16 +234,17 @@ constexpr int threads_of() { return TPR < 128 ? 128 : TPR; }
 template <int TPR>
 constexpr int fwd_ctas() { return 1024 / threads_of<TPR>(); }
 template <int TPR>
-constexpr int bwd_ctas() { return TPR >= 1024 ? 1 : 768 / threads_of<TPR>(); }
+constexpr int bwd_ctas() { return TPR >= 1024 ? 1 : 512 / threads_of<TPR>(); }
 
-template <typename T, int TPR, bool kVec>
+template <typename T, int TPR, bool kVec, int kAct>
 __global__ void __launch_bounds__(threads_of<TPR>(), fwd_ctas<TPR>())
 block_norm_kernel(const BlockNormArgs p) {
     constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
     extern __shared__ __align__(16) float sw[];
-    __shared__ float slots[2 * THREADS / 32];
+    __shared__ float2 slots[2 * THREADS / 32];
     RowSum<TPR> row_sum{slots};
     const int D = p.D, sub = threadIdx.x / TPR, c = (threadIdx.x % TPR) * E, left = D - c;
+    const float inv_w = 1.f / (float)(p.W ? p.W : 1), inv_d = 1.f / (float)D;
     const long long step = (long long)gridDim.x * RPC;
     long long r = (long long)blockIdx.x * RPC + sub;
     // the first row is requested before the weights are waited for, every other one a row ahead
@@ -202,7 +253,7 @@ block_norm_kernel(const BlockNormArgs p) {
         const int l = row < p.rows ? left : 0;
         const size_t at = (size_t)(row < p.rows ? row : 0) * D + c;
         y.load(p.y, at, l);
-        if (p.gate) z.load(p.gate, at, l);
+        if constexpr (kAct != kActNone) z.load(p.gate, at, l);
         if (p.x) x.load(p.x, at, l);
     };
     z.clear();
@@ -220,7 +271,7 @@ block_norm_kernel(const BlockNormArgs p) {
         if (r0 + step < p.rows) request(r + step, ny, nz, nx);
         float h[E], v[E];
         if (p.W) {
-            const float r1 = first_norm<T, TPR, kVec>(p, y, row_sum);
+            const float r1 = first_norm<T, TPR, kVec>(p, y, inv_w, row_sum);
             take<kVec>(w.post, c, left, v);
 #pragma unroll
             for (int i = 0; i < E; ++i) h[i] = y[i] * r1 * v[i];
@@ -228,9 +279,9 @@ block_norm_kernel(const BlockNormArgs p) {
 #pragma unroll
             for (int i = 0; i < E; ++i) h[i] = y[i];
         }
-        if (p.gate) {
+        if constexpr (kAct != kActNone) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) h[i] *= gate_of(p, z[i]);
+            for (int i = 0; i < E; ++i) h[i] *= gate_of<T, kAct>(z[i]);
         }
         if (p.r) {
             take<kVec>(w.s, c, left, v);
@@ -245,7 +296,7 @@ block_norm_kernel(const BlockNormArgs p) {
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < E; ++i) ss += h[i] * h[i];
-            const float r2 = rsqrtf(row_sum(ss) / (float)D + p.eps);
+            const float r2 = rsqrtf(row_sum(ss) * inv_d + p.eps);
             if (p.w_pre) {
                 take<kVec>(w.pre, c, left, v);
 #pragma unroll
@@ -262,46 +313,65 @@ block_norm_kernel(const BlockNormArgs p) {
     }
 }
 
-template <typename T, int TPR, bool kVec>
+template <typename T, int TPR, bool kVec, int kAct>
 __global__ void __launch_bounds__(threads_of<TPR>(), bwd_ctas<TPR>())
 block_norm_bwd_kernel(const BlockNormArgs p, const BlockNormGrads g) {
     constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
     extern __shared__ __align__(16) float sw[];
-    __shared__ float slots[2 * THREADS / 32];
+    __shared__ float2 slots[2 * THREADS / 32];
     RowSum<TPR> row_sum{slots};
     const int D = p.D, sub = threadIdx.x / TPR, c = (threadIdx.x % TPR) * E, left = D - c;
+    const float inv_w = 1.f / (float)(p.W ? p.W : 1), inv_d = 1.f / (float)D;
     float dwp[E], dwn[E], dr[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) dwp[i] = dwn[i] = dr[i] = 0.f;
     Weights w;
     w.load(p, sw);
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < p.rows; r0 += (long long)gridDim.x * RPC) {
+    const long long step = (long long)gridDim.x * RPC;
+    // (2-byte types: the next row's arrays wait in 20 registers while this one is worked on)
+    constexpr bool kAhead = sizeof(T) == 2 && kVec;
+    constexpr bool kGate = kAct != kActNone, silu = kAct == kActSilu;
+    Raw<T, kVec> y, z, x, rh, rn, ny, nz, nx, nrh, nrn;
+    auto request = [&](long long row, Raw<T, kVec>& y, Raw<T, kVec>& z, Raw<T, kVec>& x, Raw<T, kVec>& rh,
+                       Raw<T, kVec>& rn) {
+        const int l = row < p.rows ? left : 0;
+        const size_t at = (size_t)(row < p.rows ? row : 0) * D + c;
+        y.load(p.y, at, l);
+        if constexpr (kGate) z.load(p.gate, at, l);
+        if (g.dn) rn.load(g.dn, at, l);
+        if (g.dn && p.x) x.load(p.x, at, l);
+        if (g.dh) rh.load(g.dh, at, l);
+    };
+    z.clear(); x.clear(); rh.clear(); rn.clear();
+    nz.clear(); nx.clear(); nrh.clear(); nrn.clear();
+    if constexpr (kAhead) request((long long)blockIdx.x * RPC + sub, ny, nz, nx, nrh, nrn);
+    for (long long r0 = (long long)blockIdx.x * RPC; r0 < p.rows; r0 += step) {
         const long long r = r0 + sub;
         const int l = r < p.rows ? left : 0;
         const size_t at = (size_t)(r < p.rows ? r : 0) * D + c;
-        Raw<T, kVec> y, z, x, rh, rn;
-        z.clear();
-        x.clear();
-        rh.clear();
-        y.load(p.y, at, l);
-        if (p.gate) z.load(p.gate, at, l);
-        if (g.dn) {
-            rn.load(g.dn, at, l);
-            if (p.x) x.load(p.x, at, l);
+        if constexpr (kAhead) {
+            y = ny; z = nz; x = nx; rh = nrh; rn = nrn;
+            if (r0 + step < p.rows) request(r + step, ny, nz, nx, nrh, nrn);
+        } else {
+            request(r, y, z, x, rh, rn);
         }
-        if (g.dh) rh.load(g.dh, at, l);
-        // the forward's values (in registers: u, and the gate's factor where it is used)
-        float r1 = 1.f, u[E], v[E], dh[E];
+        // the forward's values again: yhat, the gate's logistic and its complement, s
+        float r1 = 1.f, yh[E], sg[E], sm[E], s[E], v[E], dh[E];
         if (p.W) {
-            r1 = first_norm<T, TPR, kVec>(p, y, row_sum);
-            take<kVec>(w.post, c, left, v);
+            r1 = first_norm<T, TPR, kVec>(p, y, inv_w, row_sum);
 #pragma unroll
-            for (int i = 0; i < E; ++i) u[i] = y[i] * r1 * v[i];
+            for (int i = 0; i < E; ++i) yh[i] = y[i] * r1;
         } else {
 #pragma unroll
-            for (int i = 0; i < E; ++i) u[i] = y[i];
+            for (int i = 0; i < E; ++i) yh[i] = y[i];
         }
-        float s[E];
+        float wp[E];
+        if (p.W) {
+            take<kVec>(w.post, c, left, wp);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) wp[i] = 1.f;
+        }
         if (p.r) {
             take<kVec>(w.s, c, left, s);
         } else {
@@ -309,9 +379,15 @@ block_norm_bwd_kernel(const BlockNormArgs p, const BlockNormGrads g) {
             for (int i = 0; i < E; ++i) s[i] = p.scale;
         }
 #pragma unroll
-        for (int i = 0; i < E; ++i) dh[i] = rh[i];
+        for (int i = 0; i < E; ++i) {
+            dh[i] = rh[i];
+            const float2 g2 = kGate ? sigmoid2<T>(z[i]) : make_float2(1.f, 0.f);
+            sg[i] = g2.x;
+            sm[i] = g2.y;
+        }
         if (g.dn) {
-            float ss = 0.f, dd = 0.f, h[E];
+            float h[E];
+            float2 t = make_float2(0.f, 0.f);                     // h^2, dn w h
             if (p.w_pre) {
                 take<kVec>(w.pre, c, left, v);
             } else {
@@ -320,53 +396,39 @@ block_norm_bwd_kernel(const BlockNormArgs p, const BlockNormGrads g) {
             }
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                h[i] = x[i] + s[i] * u[i] * (p.gate ? gate_of(p, z[i]) : 1.f);
-                ss += h[i] * h[i];
-                dd += rn[i] * v[i] * h[i];
+                v[i] *= rn[i];
+                h[i] = x[i] + s[i] * (yh[i] * wp[i] * (silu ? z[i] * sg[i] : sg[i]));
+                t.x += h[i] * h[i];
+                t.y += v[i] * h[i];
             }
-            const float r2 = rsqrtf(row_sum(ss) / (float)D + p.eps);
-            const float mean = row_sum(dd) * r2 / (float)D;       // mean of dn w hhat
+            t = row_sum.both(t);
+            const float r2 = rsqrtf(t.x * inv_d + p.eps), mean = t.y * r2 * inv_d;   // of dn w hhat
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const float hhat = h[i] * r2;
-                dh[i] += r2 * (rn[i] * v[i] - hhat * mean);
+                dh[i] += r2 * (v[i] - hhat * mean);
                 dwn[i] += rn[i] * hhat;
             }
         }
         if (g.dx) store_e<T, kVec>(g.dx, at, l, dh);
         // dh becomes the gradient of u; the gate's gradient goes out on the way
-        if (p.gate) {
-            float dz[E];
+        float dd = 0.f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float2 sg = sigmoid2(z[i]);
-                const bool silu = p.act == kActSilu;
-                const float f = silu ? z[i] * sg.x : sg.x;
-                const float slope = silu ? sg.x * (1.f + z[i] * sg.y) : sg.x * sg.y;
-                dr[i] += dh[i] * u[i] * f;
-                const float dm = dh[i] * s[i];
-                dz[i] = dm * u[i] * slope;
-                dh[i] = dm * f;
-            }
-            store_e<T, kVec>(g.dgate, at, l, dz);
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                dr[i] += dh[i] * u[i];
-                dh[i] *= s[i];
-            }
+        for (int i = 0; i < E; ++i) {
+            const float u = yh[i] * wp[i], f = silu ? z[i] * sg[i] : sg[i];
+            dr[i] += dh[i] * (u * f);
+            dh[i] *= s[i];
+            if constexpr (kGate) v[i] = dh[i] * u * (silu ? sg[i] + f * sm[i] : sg[i] * sm[i]);
+            dh[i] *= f;
+            dd += dh[i] * wp[i] * yh[i];
         }
+        if constexpr (kGate) store_e<T, kVec>(g.dgate, at, l, v);
         if (p.W) {
-            float dd = 0.f;
-            take<kVec>(w.post, c, left, v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) dd += dh[i] * v[i] * (y[i] * r1);
-            const float mean = group_w_sum<TPR>(dd, p.W, D, row_sum) / (float)p.W;
+            const float mean = group_w_sum<TPR>(dd, p.W, D, row_sum) * inv_w;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const float yhat = y[i] * r1;
-                dwp[i] += dh[i] * yhat;
-                dh[i] = r1 * (dh[i] * v[i] - yhat * mean);
+                dwp[i] += dh[i] * yh[i];
+                dh[i] = r1 * (dh[i] * wp[i] - yh[i] * mean);
             }
         }
         store_e<T, kVec>(g.dy, at, l, dh);
@@ -377,8 +439,8 @@ block_norm_bwd_kernel(const BlockNormArgs p, const BlockNormGrads g) {
     float* to = g.partial;
     auto put = [&](const float v[E], int width) {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < E; ++i) fold[threadIdx.x * E + i] = v[i];
+        Vec16<float, 4>::store(fold + threadIdx.x * E, v);
+        Vec16<float, 4>::store(fold + threadIdx.x * E + 4, v + 4);
         __syncthreads();
         for (int k = threadIdx.x; k < width; k += THREADS) {
             float t = 0.f;
@@ -451,7 +513,9 @@ cudaError_t fwd_t(const BlockNormArgs& p, cudaStream_t s) {
     constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
     const long long ctas = (p.rows + RPC - 1) / RPC, most = 148ll * fwd_ctas<TPR>();
     const size_t smem = weights_floats(p) * sizeof(float);
-    auto kern = block_norm_kernel<T, TPR, kVec>;
+    auto kern = p.act == kActSilu      ? block_norm_kernel<T, TPR, kVec, kActSilu>
+                : p.act == kActSigmoid ? block_norm_kernel<T, TPR, kVec, kActSigmoid>
+                                       : block_norm_kernel<T, TPR, kVec, kActNone>;
     const cudaError_t e = room(kern, smem);
     if (e != cudaSuccess) return e;
     kern<<<(int)(ctas < most ? ctas : most), THREADS, smem, s>>>(p);
@@ -463,7 +527,9 @@ cudaError_t bwd_t(const BlockNormArgs& p, const BlockNormGrads& g, int grid, cud
     constexpr int THREADS = threads_of<TPR>();
     const size_t wb = weights_floats(p) * sizeof(float), fb = (size_t)THREADS * E * sizeof(float);
     const size_t smem = wb > fb ? wb : fb;
-    auto kern = block_norm_bwd_kernel<T, TPR, kVec>;
+    auto kern = p.act == kActSilu      ? block_norm_bwd_kernel<T, TPR, kVec, kActSilu>
+                : p.act == kActSigmoid ? block_norm_bwd_kernel<T, TPR, kVec, kActSigmoid>
+                                       : block_norm_bwd_kernel<T, TPR, kVec, kActNone>;
     const cudaError_t e = room(kern, smem);
     if (e != cudaSuccess) return e;
     kern<<<grid, THREADS, smem, s>>>(p, g);
@@ -500,7 +566,7 @@ cudaError_t launch_bwd(const BlockNormArgs& p, const BlockNormGrads& g, int grid
 // as many as run side by side.
 int block_norm_bwd_grid(long long rows, int D) {
     const int threads = threads_per_row(D) < 128 ? 128 : threads_per_row(D);
-    const long long most = 148ll * (threads >= 1024 ? 1 : 768 / threads);
+    const long long most = 148ll * (threads >= 1024 ? 1 : 512 / threads);
     const long long need = (rows + rows_per_cta(D) - 1) / rows_per_cta(D);
     return (int)(need < most ? need : most);
 }
