@@ -187,6 +187,8 @@ la_run_kernel(const LaArgs a) {
     const int H = a.sp.H;
     const int unit = blockIdx.x / H, h = blockIdx.x - unit * H;
     const UnitAt u = find_unit(a.sp, unit);
+    la_let_next_start();
+    la_wait_before();       // (returns at once in the first launch of a call)
     if (!u.ok) return;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -533,6 +535,8 @@ la_run_kernel(const LaArgs a) {
 constexpr int kScanThreads = 256;
 __global__ void __launch_bounds__(kScanThreads)
 la_scan_kernel(const LaArgs a, int elems, int parts) {
+    la_let_next_start();
+    la_wait_before();
     const LaRun& R = a.run[blockIdx.y];
     const int H = a.sp.H;
     const int sh = blockIdx.x / parts, part = blockIdx.x - sh * parts;
@@ -610,7 +614,9 @@ cudaError_t launch_t(const LaArgs& a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)S::SMEM);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(a.sp.units * a.sp.H), a.runs), S::THREADS, S::SMEM, s>>>(a);
+    const dim3 grid((unsigned)(a.sp.units * a.sp.H), a.runs);
+    if (a.after) return la_launch_after(kern, grid, S::THREADS, S::SMEM, s, a);
+    kern<<<grid, S::THREADS, S::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -670,9 +676,8 @@ int la_scan_parts(int elems) { return (elems / 4 + kScanThreads - 1) / kScanThre
 
 cudaError_t launch_la_scan(const LaArgs& a, int dk, int dv, cudaStream_t s) {
     const int elems = dk * dv, parts = la_scan_parts(elems);
-    la_scan_kernel<<<dim3((unsigned)(a.sp.n * a.sp.H * parts), a.runs), kScanThreads, 0, s>>>(
-        a, elems, parts);
-    return cudaGetLastError();
+    return la_launch_after(la_scan_kernel, dim3((unsigned)(a.sp.n * a.sp.H * parts), a.runs),
+                           kScanThreads, 0, s, a, elems, parts);
 }
 
 cudaError_t launch_la_empty(const LaArgs& a, int dk, int dv, cudaStream_t s) {

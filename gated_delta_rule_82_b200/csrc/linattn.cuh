@@ -17,6 +17,31 @@ namespace ckda {
 
 constexpr int kLaChunk = 64;      // tokens per chunk of the chunked form
 
+// Launch with programmatic stream serialisation: the grid may start while its predecessor in the
+// stream still runs, and calls la_wait_before() ahead of everything that the predecessor wrote (or
+// still reads).  The first launch of a call is an ordinary one, so the inputs are complete by then.
+template <typename... P, typename... A>
+cudaError_t la_launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                            A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kern, args...);
+}
+__device__ __forceinline__ void la_let_next_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void la_wait_before() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // How the token axis is cut: sequences (batched rows of T tokens, or packed ones) into units of
 // at most L tokens (a multiple of kLaChunk) that are worked on side by side.
 struct LaSplit {
@@ -58,6 +83,7 @@ struct LaArgs {
     int per_token;
     LaRun run[kLaMaxRuns];
     int runs;
+    int after;                   // not the first launch of the call (la_launch_after)
 };
 
 // Where a unit lies: its sequence, its first token on the token axis, its length.

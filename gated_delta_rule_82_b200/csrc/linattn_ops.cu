@@ -228,6 +228,7 @@ cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv,
     if (split) {
         if ((e = launch_la_summary(a, dk, dv, dtype, s)) != cudaSuccess) return e;
         if ((e = launch_la_scan(a, dk, dv, s)) != cudaSuccess) return e;
+        a.after = 1;
     } else if (f.sp.cu && f.hT) {
         if ((e = launch_la_empty(a, dk, dv, s)) != cudaSuccess) return e;
     }
@@ -304,6 +305,7 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
         a.runs = 2;
         if ((e = launch_la_summary(a, dk, dv, dtype, s)) != cudaSuccess) return e;
         if ((e = launch_la_scan(a, dk, dv, s)) != cudaSuccess) return e;
+        a.after = 1;
     } else if (sp.cu && b.dh0) {
         a.run[0] = rr;
         a.runs = 1;
@@ -347,6 +349,7 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     if ((e = launch_la_run(a, dv, dk, b.dg != nullptr, dtype, s)) != cudaSuccess) return e;
     a.run[0] = v;
     a.runs = 1;
+    a.after = 1;      // (nothing of it depends on the run before: they only follow each other)
     if ((e = launch_la_run(a, dk, dv, false, dtype, s)) != cudaSuccess) return e;
 
     if (G > 1 && b.tokens > 0) {

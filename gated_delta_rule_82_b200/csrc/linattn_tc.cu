@@ -24,6 +24,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "linattn.cuh"
 #include "tc_sm100.cuh"
 
@@ -275,7 +277,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     const LaRun& R = a.run[blockIdx.y];
     const int H = a.sp.H, unit = blockIdx.x / H, h = blockIdx.x - unit * H;
     const UnitAt u = find_unit(a.sp, unit);
-    if (!u.ok) return;
+    if (!u.ok) {
+        la_wait_before();       // (no grid of a call ends before the one ahead of it)
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
     const bool rev = R.reverse;
     const int n = (u.len + C - 1) / C;
@@ -323,6 +328,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = b.tmem;
+    la_let_next_start();
     if constexpr (!kSummary) {        // (one instruction per warpgroup)
         if (warp < 8) regs_down<kRegsZ>();
         else if (warp < 16) regs_up<kRegsState>();
@@ -389,6 +395,9 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (R.unit_state) init = R.unit_state + unit_state;
             else if (R.init) init = R.init + seq_state;
         }
+        // (of what a run reads, only the entering states and the outputs' places are the business of
+        // the launches before it; the inputs are complete)
+        if constexpr (!kSummary) la_wait_before();
         float2 st[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j)
@@ -1036,9 +1045,20 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
             return cudaErrorInvalidValue;
     }
     auto kern = la_tc_kernel<NP, kSummary, kF32>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    // (an attribute of the kernel on the current device: set once for each)
+    static std::atomic<unsigned long long> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)(a.sp.units * H), a.runs), S::THREADS, S::SMEM, s>>>(t);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    const dim3 grid((unsigned)(a.sp.units * H), a.runs);
+    if (a.after) return la_launch_after(kern, grid, S::THREADS, S::SMEM, s, t);
+    kern<<<grid, S::THREADS, S::SMEM, s>>>(t);
     return cudaGetLastError();
 }
 
