@@ -48,8 +48,9 @@ ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tok
     return CKDA_OK;
 }
 
-// Units that run side by side: a CTA per SM.
-constexpr int kFwdSlots = 148, kBwdSlots = 148;
+// Units that run side by side: a CTA per SM in the forward; in the backward, whose longest launch
+// holds two runs, half of that (4096 x 16 heads: 156 us; with 148 units, and two waves, 170 us).
+constexpr int kFwdSlots = 148, kBwdSlots = 74;
 
 LaSplit make_split(const Tokens& t, const int* cu, const int* cu_host, int H, int slots) {
     LaSplit sp;
