@@ -85,6 +85,12 @@ struct RunShape {
                                    (kSummary ? 0 : NW * C * 4);
 };
 
+__device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(lo_f(w), hi_f(w));
+}
+
 // Running sums of the chunk's log2 decays (fp64, kept as two floats), and the two weights of
 // every token.  One warp.
 struct GateBuf {
@@ -122,36 +128,49 @@ __device__ void chunk_gates(GateBuf* b, double g0, double g1, bool reverse, floa
     }
 }
 
-// One operand's chunk: D channels of up to C tokens, zero behind the last one.
+// One operand's chunk: D channels of up to C tokens, zero behind the last one.  bf16: asynchronous.
 template <typename T, int D, int THREADS>
 __device__ __forceinline__ void load_rows(__nv_bfloat16* dst, const T* src, long long tok, int live,
                                           int stride, int head) {
-    constexpr int LD = D + 8;
-    if constexpr (sizeof(T) == 2) {
-        constexpr int V = D / 8;
-        for (int i = threadIdx.x; i < C * V; i += THREADS) {
-            const int r = i / V, c = (i % V) * 8;
-            const bool in = r < live;
-            cp16(smem_addr(dst + r * LD + c),
-                 src + ((size_t)(tok + (in ? r : 0)) * stride + head) * D + c, in);
-        }
-    } else {
-        constexpr int V = D / 4;
-        for (int i = threadIdx.x; i < C * V; i += THREADS) {
-            const int r = i / V, c = (i % V) * 4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int LD = D + 8, V = D / 8;
+    for (int i = threadIdx.x; i < C * V; i += THREADS) {
+        const int r = i / V, c = (i % V) * 8;
+        const bool in = r < live;
+        cp16(smem_addr(dst + r * LD + c),
+             src + ((size_t)(tok + (in ? r : 0)) * stride + head) * D + c, in);
+    }
+}
+// fp32: every request is on its way before the first value is split (a chunk's latency is one
+// memory round trip, not one per 16 bytes).
+template <int D, int THREADS>
+struct Fetch {
+    static constexpr int V = D / 4, N = C * V / THREADS;
+    float4 x[N];
+    __device__ __forceinline__ void request(const float* src, long long tok, int live, int stride,
+                                            int head) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * THREADS, r = i / V, c = (i % V) * 4;
+            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < live)
-                x = __ldg(reinterpret_cast<const float4*>(
+                x[k] = __ldg(reinterpret_cast<const float4*>(
                     src + ((size_t)(tok + r) * stride + head) * D + c));
+        }
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* dst) const {
+        constexpr int LD = D + 8;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = threadIdx.x + k * THREADS, r = i / V, c = (i % V) * 4;
             uint32_t a[3], b[3];
-            split2<3>(x.x, x.y, a);
-            split2<3>(x.z, x.w, b);
+            split2<3>(x[k].x, x[k].y, a);
+            split2<3>(x[k].z, x[k].w, b);
 #pragma unroll
             for (int p = 0; p < 3; ++p)
                 *reinterpret_cast<uint2*>(dst + p * C * LD + r * LD + c) = make_uint2(a[p], b[p]);
         }
     }
-}
+};
 
 // acc += A B for the leading terms, low += A B for the other pairs whose product is not below the
 // precision kept.  Two accumulators, because the tensor core's sums do not round to nearest: what
@@ -205,11 +224,33 @@ la_run_kernel(const LaArgs a) {
         const int c = chunk_at(i), live = min(C, u.len - c * C);
         const long long tok = u.tok + (long long)c * C;
         __nv_bfloat16* st = stages + (i % S::STAGES) * S::STAGE;
-        load_rows<T, DC, S::THREADS>(st, y, tok, live, H / R.yg, h / R.yg);
-        load_rows<T, DO, S::THREADS>(st + NI * S::XY, z, tok, live, H / R.zg, h / R.zg);
-        if constexpr (!kSummary)
-            load_rows<T, DC, S::THREADS>(st + NI * (S::XY + S::Z), x, tok, live, H / R.xg,
-                                         h / R.xg);
+        if constexpr (sizeof(T) == 2) {
+            load_rows<T, DC, S::THREADS>(st, y, tok, live, H / R.yg, h / R.yg);
+            load_rows<T, DO, S::THREADS>(st + NI * S::XY, z, tok, live, H / R.zg, h / R.zg);
+            if constexpr (!kSummary)
+                load_rows<T, DC, S::THREADS>(st + NI * (S::XY + S::Z), x, tok, live, H / R.xg,
+                                             h / R.xg);
+        } else {
+            // (in pieces of up to 16 requests a thread, where a small output leaves few threads)
+            Fetch<DC, S::THREADS> fy;
+            Fetch<DO, S::THREADS> fz;
+            fy.request(y, tok, live, H / R.yg, h / R.yg);
+            fz.request(z, tok, live, H / R.zg, h / R.zg);
+            if constexpr (!kSummary && Fetch<DC, S::THREADS>::N <= 8) {
+                Fetch<DC, S::THREADS> fx;
+                fx.request(x, tok, live, H / R.xg, h / R.xg);
+                fy.store(st);
+                fz.store(st + NI * S::XY);
+                fx.store(st + NI * (S::XY + S::Z));
+            } else {
+                fy.store(st);
+                fz.store(st + NI * S::XY);
+                if constexpr (!kSummary) {
+                    fy.request(x, tok, live, H / R.xg, h / R.xg);
+                    fy.store(st + NI * (S::XY + S::Z));
+                }
+            }
+        }
     };
     auto gate_pair = [&](int i, double* g0, double* g1) {
         const int c = chunk_at(i);
@@ -226,6 +267,7 @@ la_run_kernel(const LaArgs a) {
     // The state: rows r0 + gr (+ 8), columns 8 n + gc (+ 1).
     float M[DC / 8][4];
     const int rs = R.transposed ? DC : 1, cs = R.transposed ? 1 : DO;
+    const int own = (r0 + gr) * rs + gc * cs;
     const size_t st_size = (size_t)DC * DO;
     const size_t seq_state = ((size_t)u.seq * H + h) * st_size;
     const size_t unit_state = ((size_t)unit * H + h) * st_size;
@@ -238,8 +280,7 @@ la_run_kernel(const LaArgs a) {
     for (int n = 0; n < DC / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            M[n][e] = init ? init[(size_t)(r0 + gr + (e >> 1) * 8) * rs + (8 * n + gc + (e & 1)) * cs]
-                           : 0.f;
+            M[n][e] = init ? init[own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs] : 0.f;
     double decay = 0.0;
 
     if (warp == 0) {
@@ -247,17 +288,15 @@ la_run_kernel(const LaArgs a) {
         gate_pair(0, &g0, &g1);
         chunk_gates(&gates[0], g0, g1, rev, R.u_scale);
     }
-    load(0);
+    if constexpr (S::STAGES == 2) load(0);
     asm volatile("cp.async.commit_group;");
 
     for (int i = 0; i < nch; ++i) {
         const int c = chunk_at(i), live = min(C, u.len - c * C);
         const long long tok = u.tok + (long long)c * C;
         if constexpr (S::STAGES == 1) {
-            if (i > 0) {
-                __syncthreads();          // the last chunk's operands are done with
-                load(i);
-            }
+            if (i > 0) __syncthreads();   // the last chunk's operands are done with
+            load(i);
         }
         double g0 = 0.0, g1 = 0.0;
         if (warp == 0 && i + 1 < nch) gate_pair(i + 1, &g0, &g1);
@@ -275,11 +314,14 @@ la_run_kernel(const LaArgs a) {
         float acc[4][2][4], low[4][2][4];     // (low stays zero, and free, without lower terms)
         if constexpr (!kSummary) {
             // 1. this warp's tiles of P (16 x 16; on the kept side of the diagonal)
+            // (rolled where registers allow it: unrolled throughout, the code is 100 KB, which no
+            // instruction cache keeps from one chunk to the next)
+#pragma unroll 1
             for (int t = warp; t < 16; t += NW) {
                 const int mi = t & 3, nj = t >> 2;
                 if (rev ? mi > nj : mi < nj) continue;
                 float p[2][4] = {}, pl[2][4] = {};
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < KC; ++kk) {
                     uint32_t fa[NI][4], fb[NI][4];
 #pragma unroll
@@ -368,7 +410,7 @@ la_run_kernel(const LaArgs a) {
         if constexpr (!kSummary) {
             // 3. the chunk's own products, 16 tokens of z at a time.  z^T tile: registers 0, 2 are
             // channels 0-7, 1, 3 channels 8-15; 2, 3 tokens 8-15
-#pragma unroll
+#pragma unroll 1
             for (int kk = 0; kk < C / 16; ++kk) {
                 uint32_t fz[NI][4], b[2][NI][2];
 #pragma unroll
@@ -393,33 +435,40 @@ la_run_kernel(const LaArgs a) {
         decay += gb.sum;
         if constexpr (!kSummary) {
             // 4. the outputs: rows m 16 + gr (+ 8), channels r0 + 8 n + gc (+ 1)
+            const size_t at0 = ((size_t)tok * H + h) * DO + r0 + gc, ostep = (size_t)H * DO;
+            const int Hd = H / R.dg;
+            const T* w0 = R.dot ? static_cast<const T*>(R.dot) + ((size_t)tok * Hd + h / R.dg) * DO + r0 + gc
+                                : nullptr;
+            const bool f32 = sizeof(T) == 4 || R.out_f32;
 #pragma unroll
             for (int m = 0; m < 4; ++m)
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {
                     const int row = m * 16 + gr + e2 * 8;
-                    float dot = 0.f;
-                    if (row < live) {
-                        const size_t at = ((size_t)(tok + row) * H + h) * DO + r0 + gc;
+                    float2 v[2];
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const float v0 = acc[m][n][2 * e2] + low[m][n][2 * e2];
-                            const float v1 = acc[m][n][2 * e2 + 1] + low[m][n][2 * e2 + 1];
-                            if (sizeof(T) == 4 || R.out_f32)
-                                *reinterpret_cast<float2*>(static_cast<float*>(R.out) + at + 8 * n) =
-                                    make_float2(v0, v1);
-                            else
-                                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(R.out) + at +
-                                                             8 * n) = pack2(v0, v1);
-                            if (R.dot) {
-                                const T* w = static_cast<const T*>(R.dot) +
-                                             ((size_t)(tok + row) * (H / R.dg) + h / R.dg) * DO + r0 +
-                                             gc + 8 * n;
-                                dot += v0 * to_f32(w[0]) + v1 * to_f32(w[1]);
-                            }
+                    for (int n = 0; n < 2; ++n)
+                        v[n] = make_float2(acc[m][n][2 * e2] + low[m][n][2 * e2],
+                                           acc[m][n][2 * e2 + 1] + low[m][n][2 * e2 + 1]);
+                    if (row < live) {
+                        const size_t at = at0 + row * ostep;
+                        if (f32) {
+                            float* o = static_cast<float*>(R.out) + at;
+                            *reinterpret_cast<float2*>(o) = v[0];
+                            *reinterpret_cast<float2*>(o + 8) = v[1];
+                        } else {
+                            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(R.out) + at;
+                            *reinterpret_cast<uint32_t*>(o) = pack2(v[0].x, v[0].y);
+                            *reinterpret_cast<uint32_t*>(o + 8) = pack2(v[1].x, v[1].y);
                         }
                     }
-                    if (R.dot) {
+                    if (w0) {
+                        float dot = 0.f;
+                        if (row < live) {
+                            const T* w = w0 + (size_t)row * Hd * DO;
+                            const float2 a = pair_of(w), b = pair_of(w + 8);
+                            dot = v[0].x * a.x + v[0].y * a.y + v[1].x * b.x + v[1].y * b.y;
+                        }
                         dot += __shfl_xor_sync(0xffffffffu, dot, 1);
                         dot += __shfl_xor_sync(0xffffffffu, dot, 2);
                         if ((lane & 3) == 0) sDot[warp * C + row] = dot;
@@ -504,7 +553,7 @@ la_run_kernel(const LaArgs a) {
         for (int n = 0; n < DC / 8; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                fin[(size_t)(r0 + gr + (e >> 1) * 8) * rs + (8 * n + gc + (e & 1)) * cs] = M[n][e];
+                fin[own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs] = M[n][e];
     }
     if (kSummary && tid == 0) R.unit_decay[(size_t)unit * H + h] = decay;
     if (!kSummary && !R.unit_state && R.fin_dot) {
@@ -514,8 +563,7 @@ la_run_kernel(const LaArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 d += (double)M[n][e] *
-                     (double)R.fin_dot[seq_state + (size_t)(r0 + gr + (e >> 1) * 8) * rs +
-                                       (8 * n + gc + (e & 1)) * cs];
+                     (double)R.fin_dot[seq_state + own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         __syncthreads();                  // (the gate buffers are free)
