@@ -271,9 +271,10 @@ la_run_kernel(const LaArgs a) {
     const size_t st_size = (size_t)DC * DO;
     const size_t seq_state = ((size_t)u.seq * H + h) * st_size;
     const size_t unit_state = ((size_t)unit * H + h) * st_size;
+    const bool fold = !kSummary && R.fold;
     const float* init = nullptr;
     if (!kSummary) {
-        if (R.unit_state) init = R.unit_state + unit_state;
+        if (R.unit_state && !fold) init = R.unit_state + unit_state;
         else if (R.init) init = R.init + seq_state;
     }
 #pragma unroll
@@ -281,6 +282,20 @@ la_run_kernel(const LaArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             M[n][e] = init ? init[own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs] : 0.f;
+    if (fold) {                               // the units ahead of this one, in the run's order
+        const int ahead = rev ? u.count - 1 - u.index : u.index;
+#pragma unroll 1
+        for (int k = 0; k < ahead; ++k) {
+            const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;
+            const float w = exp2f((float)R.unit_decay[un]);
+            const float* E = R.unit_state + un * st_size + own;
+#pragma unroll
+            for (int n = 0; n < DC / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    M[n][e] = fmaf(M[n][e], w, E[(e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs]);
+        }
+    }
     double decay = 0.0;
 
     if (warp == 0) {
@@ -546,8 +561,9 @@ la_run_kernel(const LaArgs a) {
     }
 
     // the state after the unit: a summary, or (one unit per sequence) the final state
-    float* fin = kSummary ? R.unit_state + unit_state
-                          : (!R.unit_state && R.fin ? R.fin + seq_state : nullptr);
+    // (the run's last unit of a sequence, where no scan has formed it)
+    const bool last = !R.unit_state || (fold && u.index == (rev ? 0 : u.count - 1));
+    float* fin = kSummary ? R.unit_state + unit_state : (last && R.fin ? R.fin + seq_state : nullptr);
     if (fin) {
 #pragma unroll
         for (int n = 0; n < DC / 8; ++n)
@@ -556,7 +572,7 @@ la_run_kernel(const LaArgs a) {
                 fin[own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs] = M[n][e];
     }
     if (kSummary && tid == 0) R.unit_decay[(size_t)unit * H + h] = decay;
-    if (!kSummary && !R.unit_state && R.fin_dot) {
+    if (!kSummary && last && R.fin_dot) {
         double d = 0.0;
 #pragma unroll
         for (int n = 0; n < DC / 8; ++n)

@@ -25,21 +25,24 @@ bool overlap(const Buf& a, const Buf& b) {
 struct Tokens {
     int n, T;              // sequences; tokens of a row (batched) or of the axis (packed)
     long long total, longest;
+    int empty;             // a packed sequence has no tokens
 };
 ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tokens* t) {
     if (!cu_host) {
         if (B < 1 || T < 1 || H < 1) return CKDA_ERR_SHAPE;
-        *t = Tokens{B, T, (long long)B * T, T};
+        *t = Tokens{B, T, (long long)B * T, T, 0};
     } else {
         if (n_seqs < 1 || H < 1) return CKDA_ERR_SHAPE;
         if (cu_host[0] != 0) return CKDA_ERR_ARG;
         long long longest = 0;
+        int empty = 0;
         for (int s = 0; s < n_seqs; ++s) {
             const long long len = (long long)cu_host[s + 1] - cu_host[s];
             if (len < 0) return CKDA_ERR_ARG;
             longest = len > longest ? len : longest;
+            empty |= len == 0;
         }
-        *t = Tokens{n_seqs, cu_host[n_seqs], (long long)cu_host[n_seqs], longest};
+        *t = Tokens{n_seqs, cu_host[n_seqs], (long long)cu_host[n_seqs], longest, empty};
     }
     // (grid sizes and chunk numbers stay below 2^31, byte counts below 2^48)
     if (t->longest > 0x7fffff00ll) return CKDA_ERR_SHAPE;   // (rounded up to whole chunks below 2^31)
@@ -58,6 +61,7 @@ LaSplit make_split(const Tokens& t, const int* cu, const int* cu_host, int H, in
     sp.n = t.n;
     sp.T = t.T;
     sp.H = H;
+    sp.empty = t.empty;
     sp.L = la_unit_len(t.total, t.longest, H, slots);
     sp.units = (int)la_units(cu_host, t.n, t.T, sp.L);
     return sp;

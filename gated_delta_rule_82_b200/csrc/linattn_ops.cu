@@ -197,8 +197,11 @@ FwdWs fwd_ws(void* ws, bool split, long long units, int H, int dk, int dv) {
     w.bytes = c.at;
     return w;
 }
-// more than one unit in a sequence
+// more than one unit in a sequence; few enough for the runs to add the summaries up themselves
 bool is_split(const LaSplit& sp, long long longest) { return longest > sp.L; }
+bool is_folded(const LaSplit& sp, long long longest) {
+    return (longest + sp.L - 1) / sp.L <= kLaFoldUnits;
+}
 }  // namespace
 
 size_t la_fwd_workspace(const LaSplit& sp, long long longest, int dk, int dv) {
@@ -223,14 +226,15 @@ cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv,
     r.p_scale = r.o_scale = f.scale;
     r.unit_state = w.states;
     r.unit_decay = w.decay;
+    r.fold = is_folded(f.sp, longest);
     a.run[0] = r;
     cudaError_t e;
+    if (f.sp.empty && f.hT && (!split || r.fold))
+        if ((e = launch_la_empty(a, dk, dv, s)) != cudaSuccess) return e;
     if (split) {
         if ((e = launch_la_summary(a, dk, dv, dtype, s)) != cudaSuccess) return e;
-        if ((e = launch_la_scan(a, dk, dv, s)) != cudaSuccess) return e;
         a.after = 1;
-    } else if (f.sp.cu && f.hT) {
-        if ((e = launch_la_empty(a, dk, dv, s)) != cudaSuccess) return e;
+        if (!r.fold && (e = launch_la_scan(a, dk, dv, s)) != cudaSuccess) return e;
     }
     return launch_la_run(a, dk, dv, false, dtype, s);
 }
@@ -293,23 +297,24 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     rr.fin = b.dh0;
     rr.reverse = 1;
     rr.u_scale = b.scale;
-    rs.fin_dot = rr.fin_dot = nullptr;
     const bool want_dot = b.dg && b.dhT;
+    const bool fold = is_folded(sp, longest), scan = split && !fold;
     int parts = 1;
+    if (sp.empty && b.dh0 && !scan) {
+        a.run[0] = rr;
+        a.runs = 1;
+        if ((e = launch_la_empty(a, dk, dv, s)) != cudaSuccess) return e;
+    }
     if (split) {
         rs.unit_state = w.S; rs.unit_decay = w.decS;
         rr.unit_state = w.R; rr.unit_decay = w.decR;
-        if (want_dot) { rs.fin_dot = b.dhT; rs.fin_dot_out = w.dot; parts = la_scan_parts(dk * dv); }
+        if (scan && want_dot) { rs.fin_dot = b.dhT; rs.fin_dot_out = w.dot; parts = la_scan_parts(dk * dv); }
         a.run[0] = rs;
         a.run[1] = rr;
         a.runs = 2;
         if ((e = launch_la_summary(a, dk, dv, dtype, s)) != cudaSuccess) return e;
-        if ((e = launch_la_scan(a, dk, dv, s)) != cudaSuccess) return e;
         a.after = 1;
-    } else if (sp.cu && b.dh0) {
-        a.run[0] = rr;
-        a.runs = 1;
-        if ((e = launch_la_empty(a, dk, dv, s)) != cudaSuccess) return e;
+        if (scan && (e = launch_la_scan(a, dk, dv, s)) != cudaSuccess) return e;
     }
 
     LaRun q = blank_run(), k = blank_run(), v = blank_run();
@@ -318,15 +323,16 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     q.transposed = 1;
     q.p_scale = q.o_scale = b.scale;
     q.init = b.h0;
-    q.unit_state = w.S;
-    if (!split && want_dot) { q.fin_dot = b.dhT; q.fin_dot_out = w.dot; }
+    q.unit_state = w.S; q.unit_decay = w.decS;
+    q.fold = k.fold = v.fold = fold;
+    if (!scan && want_dot) { q.fin_dot = b.dhT; q.fin_dot_out = w.dot; }
     k.x = b.v; k.y = b.dout; k.z = b.q; k.zg = G;
     k.out = G > 1 ? (void*)w.dkf : b.dk;
     k.transposed = 1;
     k.reverse = 1;
     k.p_scale = k.u_scale = b.scale;
     k.init = b.dhT;
-    k.unit_state = w.R;
+    k.unit_state = w.R; k.unit_decay = w.decR;
     q.out_f32 = k.out_f32 = G > 1;
     if (b.dg) {
         q.dot = b.q; k.dot = b.k;
@@ -339,8 +345,8 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     v.reverse = 1;
     v.p_scale = v.u_scale = b.scale;
     v.init = b.dhT;
-    v.unit_state = w.R;
-    if (!split) v.fin = b.dh0;
+    v.unit_state = w.R; v.unit_decay = w.decR;
+    if (!scan) v.fin = b.dh0;
     a.run[0] = q;
     a.run[1] = k;
     a.runs = 2;

@@ -390,9 +390,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const size_t seq_state = ((size_t)u.seq * H + h) * (D * D);
         const size_t unit_state = ((size_t)unit * H + h) * (D * D);
         const size_t own = (size_t)row * rs + (size_t)col0 * cs;
+        const bool fold = !kSummary && R.fold;
         const float* init = nullptr;
         if (!kSummary) {
-            if (R.unit_state) init = R.unit_state + unit_state;
+            if (R.unit_state && !fold) init = R.unit_state + unit_state;
             else if (R.init) init = R.init + seq_state;
         }
         // (of what a run reads, only the entering states and the outputs' places are the business of
@@ -403,6 +404,19 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int j = 0; j < 32; ++j)
             st[j] = init ? make_float2(init[own + (size_t)(2 * j) * cs], init[own + (size_t)(2 * j + 1) * cs])
                          : make_float2(0.f, 0.f);
+        if (fold) {                               // the units ahead of this one, in the run's order
+            const int ahead = rev ? u.count - 1 - u.index : u.index;
+#pragma unroll 1
+            for (int k = 0; k < ahead; ++k) {
+                const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;
+                const float w = exp2f((float)R.unit_decay[un]);
+                const float* E = R.unit_state + un * (D * D) + own;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    st[j] = fma2(st[j], make_float2(w, w),
+                                 make_float2(E[(size_t)(2 * j) * cs], E[(size_t)(2 * j + 1) * cs]));
+            }
+        }
         bool ok = true;
         auto put_state = [&](int i) {             // the state entering chunk i, as an operand
             if (i > 0 && !wait(b, &b.s_empty, (i - 1) & 1)) return false;
@@ -602,8 +616,9 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         }
         if (!kSummary && lane == 0) tc::bulk_wait_all();
         if (ok) {
-            float* fin = kSummary ? R.unit_state + unit_state
-                                  : (!R.unit_state && R.fin ? R.fin + seq_state : nullptr);
+            // the run's last unit of a sequence leaves the final state (where no scan has formed it)
+            const bool last = !R.unit_state || (fold && u.index == (rev ? 0 : u.count - 1));
+            float* fin = kSummary ? R.unit_state + unit_state : (last && R.fin ? R.fin + seq_state : nullptr);
             if (fin) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
@@ -611,7 +626,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                     fin[own + (size_t)(2 * j + 1) * cs] = st[j].y;
                 }
             }
-            if (!kSummary && !R.unit_state && R.fin_dot) {
+            if (!kSummary && last && R.fin_dot) {
                 const float* f = R.fin_dot + seq_state + own;
                 double d = 0.0;
 #pragma unroll
