@@ -17,8 +17,10 @@
 // Precision: every value enters the products as a sum of bf16 terms: one for a bf16 input
 // (exact), three for an fp32 one (8 bits each, 24 in all; the products of terms below 2^-24 are
 // left out).  The weighted z of the state update always has three, so states are fp32-grade
-// whatever the input type; P and M as operands have three when `exact` asks for it, else one
-// (rounded to bf16, as the bf16 output is).
+// whatever the input type; P and M as operands have three when `exact` asks for it, else P two and M
+// one: of the operands of a bf16 output only the state is rounded to bf16.  (With one term of P too,
+// outputs that are small differences of the chunk's own part and the state's had 1.6 times the error
+// of their own rounding.)
 #include "linattn.cuh"
 
 namespace ckda {
@@ -80,7 +82,8 @@ struct RunShape {
     static constexpr int LC = DC + 8, LO = DO + 8, LP = C + 8;   // row pitches: 16 bytes of padding
     static constexpr int XY = C * LC, Z = C * LO;      // (elements; keeps ldmatrix conflict-free)
     static constexpr int STAGE = NI * (XY * (kSummary ? 1 : 2) + Z);
-    static constexpr int PP = kSummary ? 0 : NP * C * LP;
+    static constexpr int PT = NP == 1 ? 2 : NP;        // terms of P
+    static constexpr int PP = kSummary ? 0 : PT * C * LP;
     static constexpr size_t SMEM = (size_t)(STAGES * STAGE + PP) * 2 + 2 * (4 * C + 8) * 4 +
                                    (kSummary ? 0 : NW * C * 4);
 };
@@ -193,7 +196,7 @@ template <typename T, int DC, int DO, bool kSummary, int NP>
 __global__ void __launch_bounds__(DO * 2)
 la_run_kernel(const LaArgs a) {
     using S = RunShape<T, DC, DO, kSummary, NP>;
-    constexpr int NW = S::NW, NI = S::NI, LC = S::LC, LO = S::LO, LP = S::LP;
+    constexpr int NW = S::NW, NI = S::NI, LC = S::LC, LO = S::LO, LP = S::LP, PT = S::PT;
     constexpr int KC = DC / 16;                 // 16-deep steps over the contracted channels
     constexpr int NU = 3;                       // terms of the weighted z
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -371,10 +374,10 @@ la_run_kernel(const LaArgs a) {
                             const bool keep = rev ? row <= col + e : row >= col + e;
                             w[e] = keep ? (p[n][2 * e2 + e] + pl[n][2 * e2 + e]) * exp2f(rev ? -d : d) * R.p_scale : 0.f;
                         }
-                        uint32_t t3[NP];
-                        split2<NP>(w[0], w[1], t3);
+                        uint32_t t3[PT];
+                        split2<PT>(w[0], w[1], t3);
 #pragma unroll
-                        for (int q = 0; q < NP; ++q)
+                        for (int q = 0; q < PT; ++q)
                             *reinterpret_cast<uint32_t*>(sP + q * C * LP + row * LP + col) = t3[q];
                     }
             }
@@ -437,13 +440,13 @@ la_run_kernel(const LaArgs a) {
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     if (rev ? m > kk : m < kk) continue;
-                    uint32_t fp[NP][4];
+                    uint32_t fp[PT][4];
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
+                    for (int q = 0; q < PT; ++q)
                         ldsm4(fp[q], smem_addr(sP + q * C * LP + (m * 16 + (lane & 15)) * LP +
                                                kk * 16 + (lane >> 4) * 8));
-                    mma_terms<NP, NI>(acc[m][0], low[m][0], fp, b[0]);
-                    mma_terms<NP, NI>(acc[m][1], low[m][1], fp, b[1]);
+                    mma_terms<PT, NI>(acc[m][0], low[m][0], fp, b[0]);
+                    mma_terms<PT, NI>(acc[m][1], low[m][1], fp, b[1]);
                 }
             }
         }
@@ -731,6 +734,9 @@ cudaError_t launch_la_summary(const LaArgs& a, int dc, int dout, ckda_dtype dtyp
 cudaError_t launch_la_run(const LaArgs& a, int dc, int dout, bool exact, ckda_dtype dtype,
                           cudaStream_t s) {
     if (a.sp.units == 0) return cudaSuccess;
+    // A few outputs have no averages to hide a rounded state in, and in a run of a few chunks full
+    // precision costs little (one 64-token chunk on 16 heads: 7.4 -> 9.0 us).
+    if ((long long)a.sp.units * a.sp.H * (a.sp.L / kLaChunk) <= 64) exact = true;
     if (dtype == CKDA_BF16 && dc == 128 && dout == 128) return launch_la_tc_run(a, exact, s);
     return dtype == CKDA_BF16 ? launch_type<__nv_bfloat16>(a, dc, dout, false, exact, s)
                               : launch_type<float>(a, dc, dout, false, true, s);

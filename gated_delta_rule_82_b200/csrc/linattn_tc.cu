@@ -10,7 +10,8 @@
 // X, Y, Z arrive by TMA as 128-byte-swizzled tiles; one tile serves as K-major and as MN-major
 // operand.  The state lives in the registers of eight warps (a row of 64 channels per thread) and
 // goes to the tensor core as a bf16 operand through TMEM; the weighted Z as well, in three bf16
-// terms (24 bits, 32 columns each), so that states are fp32-grade.  With NP = 3 the
+// terms (24 bits, 32 columns each), so that states are fp32-grade.  P has two terms, so that of the
+// operands only the state is rounded to bf16 (the output's own rounding comes on top).  With NP = 3 the
 // scores and the state enter in three terms too (the state's second and third from shared memory).
 //
 // Roles (one CTA per SM, all of TMEM): warps 0-7 weight Z; 8-15 carry the state and write the
@@ -18,7 +19,7 @@
 // TMA), and O1 with O2 (a poll of a barrier takes 80 cycles even when it is complete, so one warp
 // that issued all of them would be the slowest part).  They meet on mbarriers only, so a chunk's
 // products overlap the neighbours' element work: per chunk the tensor pipe needs 256 (Sc) + 768 (U)
-// + 256 (O1) + 200 (O2) cycles at NP = 1.
+// + 256 (O1) + 400 (O2) cycles at NP = 1.
 // Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
 // once its copies and products have landed.
 #include <cuda.h>
@@ -76,7 +77,8 @@ struct TcShape {
     static constexpr int STAGES = kSummary ? 4 : NP == 1 ? 3 : 2;
     static constexpr int STAGE = kSummary ? 2 * kTile : 3 * kTile;       // Y, Z, X
     static constexpr int PBUF = NP == 1 ? 2 : 1;                         // buffers of P
-    static constexpr int P = kSummary ? 0 : PBUF * NP * kBlock;
+    static constexpr int PT = NP == 1 ? 2 : NP;                          // terms of P
+    static constexpr int P = kSummary ? 0 : PBUF * PT * kBlock;
     static constexpr int OUT = kSummary ? 0 : 2 * kTile;                 // outputs on their way out
     static constexpr int SLO = kSummary ? 0 : (NP - 1) * D * D * 2;      // lower terms of the state
     static constexpr int GATES = STAGES * STAGE + P + SLO + OUT;
@@ -257,9 +259,9 @@ __device__ __forceinline__ uint32_t stage_at(uint32_t tok, uint32_t piece) {
     return tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4);
 }
 
-// kF32: the outputs are fp32 (gradients that are still to be summed over a group of heads).  NP = 3
-// goes with products of the output rows (the decay gradient's need for precision is why it exists).
-template <int NP, bool kSummary, bool kF32>
+// kF32: the outputs are fp32 (gradients that are still to be summed over a group of heads).
+// kDots: the output rows are multiplied with LaRun::dot.
+template <int NP, bool kSummary, bool kF32, bool kDots>
 __global__ void __launch_bounds__(TcShape<NP, kSummary>::THREADS, 1)
 la_tc_kernel(const __grid_constant__ TcArgs args) {
     using S = TcShape<NP, kSummary>;
@@ -458,7 +460,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
         const int m4 = lane >> 3;                                // matrix of an x4 access
         uint8_t* sOut0 = sSlo + S::SLO + (warp - 8) * (kTile / 8);      // two areas, a tile apart
-        constexpr bool dots = !kSummary && NP > 1;
+        constexpr bool dots = kDots;
         // The rows that the outputs are multiplied with, into the staging area, long before their use.
         auto fetch_rows = [&](int i) {
             const int Hd = H / R.dg, live = live_of(i) - tq;
@@ -646,11 +648,11 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         }
     } else if (!kSummary && warp < S::EXTRA) {
         // -------------------------------------------------------------------- P from the scores
-        constexpr int PB = S::PBUF;
+        constexpr int PB = S::PBUF, PT = S::PT;
         const int gr = lane >> 2, gc = 2 * (lane & 3);
         const float p_scale = R.p_scale;
         // P is zero beyond the diagonal: those 16 x 8 tiles are cleared once and stay
-        for (int k = 0; k < PB * NP; ++k)
+        for (int k = 0; k < PB * PT; ++k)
             for (int w = lane; w < 16 * 8; w += 32) {
                 const int row = 16 * quarter + (w >> 3), c8 = w & 7;
                 if (rev ? c8 < 2 * quarter : c8 > 2 * quarter + 1)
@@ -665,9 +667,9 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
+                    for (int q = 0; q < PT; ++q)       // (two terms: the second rounds what is left)
                         *reinterpret_cast<uint32_t*>(p + q * kBlock + e * 1024 + at) =
-                            NP == 1 ? pack2(w[2 * j + e].x, w[2 * j + e].y) : cut2(w[2 * j + e]);
+                            PT == 2 && q == 1 ? pack2(w[2 * j + e].x, w[2 * j + e].y) : cut2(w[2 * j + e]);
             }
         };
         auto make_p = [&](int i) {
@@ -688,7 +690,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (i >= PB && !wait(b, &b.p_empty[buf], (i / PB - 1) & 1)) return false;
             tc::tc_fence_after();
             const uint32_t sc = tc::tmem_addr(tmem, 32 * quarter, kColSc);
-            uint8_t* p = sP + buf * NP * kBlock + r0 * 128 + gc * 2;
+            uint8_t* p = sP + buf * PT * kBlock + r0 * 128 + gc * 2;
             float2 x[4], nx[4];
             tmem_ld_16x16(sc + 16 * quarter, x);
             // the diagonal tile, while the first of the others is on its way (outwards from it)
@@ -740,7 +742,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     } else if (warp == S::EXTRA) {
         // -------------------------------------------------------------------------- the decays
         // (and the output rows' products: their sums over the channel groups, and over the chunk)
-        constexpr bool dots = !kSummary && NP > 1;
+        constexpr bool dots = kDots;
         auto dot_rows = [&](int i) {
             const int slot = i % kGateRing;
             const float* d = sDot + 4 * slot * C;
@@ -983,13 +985,13 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 const uint64_t zd = tc::desc_add(zd0, at.slot * S::STAGE);
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int q = NP - 1; q >= 0; --q) {
+                    for (int q = S::PT - 1; q >= 0; --q) {
                         const uint64_t pd =
-                            tc::smem_desc_sw128(tc::smem_u32(sP) + (pb.slot * NP + q) * kBlock, 16, 1024);
+                            tc::smem_desc_sw128(tc::smem_u32(sP) + (pb.slot * S::PT + q) * kBlock, 16, 1024);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             tc::mma_bf16(tmem + kColO2, tc::desc_add(zd, ks * 2048),
-                                         tc::desc_add(pd, ks * 32), id_o2, q < NP - 1 || ks > 0);
+                                         tc::desc_add(pd, ks * 32), id_o2, q < S::PT - 1 || ks > 0);
                     }
                     tc::mma_commit(&b.p_empty[pb.slot]);
                     tc::mma_commit(&b.o_full);
@@ -1044,7 +1046,7 @@ bool encode(CUtensorMap* m, const void* base, int heads, int T, int rows, bool s
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NP, bool kSummary, bool kF32>
+template <int NP, bool kSummary, bool kF32, bool kDots>
 cudaError_t launch(const LaArgs& a, cudaStream_t s) {
     using S = TcShape<NP, kSummary>;
     TcArgs t;
@@ -1059,7 +1061,7 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
         if (!kSummary && !kF32 && !encode(&t.out[r], u.out, H, a.sp.T, rows, true))
             return cudaErrorInvalidValue;
     }
-    auto kern = la_tc_kernel<NP, kSummary, kF32>;
+    auto kern = la_tc_kernel<NP, kSummary, kF32, kDots>;
     // (an attribute of the kernel on the current device: set once for each)
     static std::atomic<unsigned long long> set{0};
     int dev = 0;
@@ -1080,12 +1082,14 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s) {
-    return launch<1, true, false>(a, s);
+    return launch<1, true, false, false>(a, s);
 }
-// (the runs of one launch agree in out_f32, and have rows to multiply with where exact is set)
+// (the runs of one launch agree in out_f32 and in having rows to multiply with; the latter are exact)
 cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s) {
-    if (a.run[0].out_f32) return exact ? launch<3, false, true>(a, s) : launch<1, false, true>(a, s);
-    return exact ? launch<3, false, false>(a, s) : launch<1, false, false>(a, s);
+    const bool f32 = a.run[0].out_f32, dots = a.run[0].dot != nullptr;
+    if (dots) return f32 ? launch<3, false, true, true>(a, s) : launch<3, false, false, true>(a, s);
+    if (exact) return f32 ? launch<3, false, true, false>(a, s) : launch<3, false, false, false>(a, s);
+    return f32 ? launch<1, false, true, false>(a, s) : launch<1, false, false, false>(a, s);
 }
 
 // Read this file's status word (`stream` has finished) and clear it.
