@@ -226,7 +226,8 @@ cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv,
     r.p_scale = r.o_scale = f.scale;
     r.unit_state = w.states;
     r.unit_decay = w.decay;
-    r.fold = is_folded(f.sp, longest);
+    // (every unit reads h0 then, and the last one writes hT: not when they are the same)
+    r.fold = is_folded(f.sp, longest) && f.hT != f.h0;
     a.run[0] = r;
     cudaError_t e;
     if (f.sp.empty && f.hT && (!split || r.fold))
