@@ -286,7 +286,7 @@ la_run_kernel(const LaArgs a) {
         for (int e = 0; e < 4; ++e)
             M[n][e] = init ? init[own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs] : 0.f;
     if (fold) {                               // the units ahead of this one, in the run's order
-        const int ahead = rev ? u.count - 1 - u.index : u.index;
+        const int ahead = rev ? min(u.count - 1 - u.index, a.sp.units - 1 - unit) : u.index;
 #pragma unroll 1
         for (int k = 0; k < ahead; ++k) {
             const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;
