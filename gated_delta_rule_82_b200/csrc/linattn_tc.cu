@@ -39,7 +39,7 @@ constexpr int D = 128;                    // contracted and output channels
 constexpr int kTile = C * D * 2;          // bytes of one operand tile
 constexpr int kBlock = C * 128;           // 64 channels of it
 constexpr int kGateRing = 4;
-constexpr int kPolls = 1 << 18;
+constexpr int kPolls = 1 << 20;
 
 // TMEM columns
 constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320;
@@ -102,7 +102,7 @@ struct Bars {
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
 // Bounded wait of a converged warp: false when it has run out (a poll sleeps for up to about 4 us,
-// so between 20 ms and a second).  Short and in line: the roles' hot code together has to stay in
+// so after some 4 s at most).  Short and in line: the roles' hot code together has to stay in
 // the instruction cache (at 50 KB the element warps spent most of their time on instruction
 // fetches), and calls do not go with the warpgroups' register shares.
 __device__ __forceinline__ bool wait(Bars& b, uint64_t* bar, uint32_t parity) {
@@ -407,7 +407,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             st[j] = init ? make_float2(init[own + (size_t)(2 * j) * cs], init[own + (size_t)(2 * j + 1) * cs])
                          : make_float2(0.f, 0.f);
         if (fold) {                               // the units ahead of this one, in the run's order
-            const int ahead = rev ? u.count - 1 - u.index : u.index;
+            const int ahead = rev ? min(u.count - 1 - u.index, a.sp.units - 1 - unit) : u.index;
 #pragma unroll 1
             for (int k = 0; k < ahead; ++k) {
                 const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;

@@ -131,6 +131,7 @@ CKDA_API const char* ckda_strerror(ckda_status status);
  *   1  a wait of the tensor-core forward's chunk-factor work ran out (a poll limit)
  *   2  a wait of the tensor-core forward's state pass ran out (ckda_set_wait_limit_ns)
  *   3  ckda_fwd_varlen: the device copy of cu_seqlens disagrees with the host copy
+ *   4  a wait of the linear attention's tensor-core kernels ran out (a poll limit, some seconds)
  * Returns CKDA_OK for 0, CKDA_ERR_DEVICE_STATUS otherwise, CKDA_ERR_CUDA when the read fails.
  * After a recorded failure the outputs of the failing call are unspecified.  There is no
  * counterpart on the pages: it reports the bounded waits of this library's own kernels.
@@ -360,7 +361,7 @@ CKDA_API ckda_status ckda_bwd_chunked(const void* q, const void* k, const void* 
  * bf16 where they enter the output's products.  No positive exponent of a decay is formed, so any
  * g <= 0 is safe; a growing g > 0 is accepted and can overflow as the recurrence does.  A
  * non-finite input reaches every later output of its head, and may reach the outputs of earlier
- * tokens of the same chunk of 64 (or 128) tokens.
+ * tokens of the same chunk of 64 tokens.
  */
 CKDA_API size_t ckda_linattn_fwd_workspace_bytes(int B, int T, const int* cu_seqlens_host,
                                                  int n_seqs, int H, int dk, int dv);
