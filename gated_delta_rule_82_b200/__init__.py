@@ -307,6 +307,8 @@ def _host_offsets(cu_seqlens, cu_seqlens_cpu):
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens: expected [n + 1] token offsets, n >= 1")
     host = cu_seqlens.cpu() if cu_seqlens_cpu is None else cu_seqlens_cpu
+    if host.device.type != "cpu":
+        raise ValueError("cu_seqlens_cpu is not on the CPU")
     host = host.to(torch.int32).contiguous()
     if tuple(host.shape) != tuple(cu_seqlens.shape):
         raise ValueError("cu_seqlens_cpu must have the shape of cu_seqlens")
@@ -684,6 +686,8 @@ def _norm_args(y, gate, gate_act, residual, post_group, post_weight, res_scale, 
         _need(gate, "gate", y.dtype, y.shape, dev)
     if residual is not None:
         _need(residual, "residual", y.dtype, y.shape, dev)
+    if gate_act not in GATE_ACTS:
+        raise ValueError(f"gate_act: expected one of {sorted(GATE_ACTS)}, got {gate_act!r}")
     if (gate is None) != (gate_act == "none"):
         raise ValueError("gate and gate_act go together (gate_act 'none' without a gate)")
     if post_weight is not None:

@@ -97,12 +97,13 @@ ckda_status ckda_linattn_fwd_chunked(const void* q, const void* k, const void* v
                                      const int* cu_seqlens_host, int n_seqs, int H, int dk, int dv,
                                      ckda_flags flags, ckda_dtype dtype, void* workspace,
                                      size_t workspace_bytes, ckda_stream_t stream) {
-    if (!q || !k || !v || !log_decay || !out) return CKDA_ERR_NULL;
     if (!cu_seqlens != !cu_seqlens_host) return CKDA_ERR_NULL;
     if (dtype != CKDA_F32 && dtype != CKDA_BF16) return CKDA_ERR_UNSUPPORTED;
     Tokens t;
     ckda_status st = read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t);
     if (st != CKDA_OK) return st;
+    if (t.total > 0 && (!q || !k || !v || !out)) return CKDA_ERR_NULL;
+    if ((t.total > 0 || !per_token) && !log_decay) return CKDA_ERR_NULL;
     if (!supported_dim(dk) || !supported_dim(dv)) return CKDA_ERR_UNSUPPORTED;
     if (per_token != 0 && per_token != 1) return CKDA_ERR_ARG;
     int G;
@@ -147,12 +148,13 @@ ckda_status ckda_linattn_bwd_chunked(const void* q, const void* k, const void* v
                                      int H, int dk_, int dv_, ckda_flags flags, ckda_dtype dtype,
                                      void* workspace, size_t workspace_bytes,
                                      ckda_stream_t stream) {
-    if (!q || !k || !v || !log_decay || !dout || !dq || !dk || !dv) return CKDA_ERR_NULL;
     if (!cu_seqlens != !cu_seqlens_host) return CKDA_ERR_NULL;
     if (dtype != CKDA_F32 && dtype != CKDA_BF16) return CKDA_ERR_UNSUPPORTED;
     Tokens t;
     ckda_status st = read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t);
     if (st != CKDA_OK) return st;
+    if (t.total > 0 && (!q || !k || !v || !dout || !dq || !dk || !dv)) return CKDA_ERR_NULL;
+    if ((t.total > 0 || !per_token) && !log_decay) return CKDA_ERR_NULL;
     if (!supported_dim(dk_) || !supported_dim(dv_)) return CKDA_ERR_UNSUPPORTED;
     if (per_token != 0 && per_token != 1) return CKDA_ERR_ARG;
     int G;

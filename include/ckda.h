@@ -344,12 +344,12 @@ CKDA_API ckda_status ckda_bwd_chunked(const void* q, const void* k, const void* 
  * normalises them).
  *   q, k      : [B, T, Hk, dk] dtype (Hk = flags.qk_heads, or H)     v, out : [B, T, H, dv] dtype
  *   log_decay : fp32, [B, T, H] (per_token = 1) or [H] (per_token = 0: fixed decays); 4-byte
-               aligned, as is its gradient (every other array 16-byte)
+ *               aligned, as is its gradient (every other array 16-byte)
  *   h0, hT    : [B, H, dk, dv] fp32; h0 may be NULL (zero), hT NULL (not wanted) or equal to h0
  *   cu_seqlens, cu_seqlens_host, n_seqs : packed sequences, as in ckda_fwd_varlen (both pointers,
  *               or both NULL): then B and T are ignored, the token axis holds
  *               cu_seqlens_host[n_seqs] tokens and h0, hT are [n_seqs, H, dk, dv].  Sequences may
- *               be empty (hT is h0, or zero).  Offsets on the device that differ from the host's
+ *               be empty (hT is h0, or zero); where all are, arrays over tokens may be NULL.  Offsets on the device that differ from the host's
  *               give undefined results within the arrays.
  *   flags     : scale and qk_heads are used, path and stages ignored; l2norm, rope_theta > 0 or
  *               gate_logits: CKDA_ERR_ARG
@@ -357,8 +357,8 @@ CKDA_API ckda_status ckda_bwd_chunked(const void* q, const void* k, const void* 
  *               calls.
  * Long sequences are cut into units of tokens worked on side by side: summaries of the units, a
  * scan over them, then every unit from its entering state.  States are kept and updated with
- * fp32-grade products for either type; with bf16 inputs the scores and the state are rounded to
- * bf16 where they enter the output's products.  No positive exponent of a decay is formed, so any
+ * fp32-grade products for either type; with bf16 inputs the state is rounded to bf16 where
+ * it enters the output's products.  No positive exponent of a decay is formed, so any
  * g <= 0 is safe; a growing g > 0 is accepted and can overflow as the recurrence does.  A
  * non-finite input reaches every later output of its head, and may reach the outputs of earlier
  * tokens of the same chunk of 64 tokens.

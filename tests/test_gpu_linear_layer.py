@@ -217,3 +217,41 @@ def test_prompt_after_other_shapes_and_last_rows():
     v[100:] = float("nan")
     out2, _ = ck.linattn_fwd_chunked(p["q"], p["k"], v, p["g"], p["h0"], cu_seqlens=cu.cuda(), cu_seqlens_cpu=cu)
     assert torch.equal(out2[:100], out[:100])
+
+
+@pytest.mark.parametrize("per_token", [True, False])
+def test_all_sequences_empty(per_token):
+    """A batch without tokens: empty outputs, states and their gradients passed through."""
+    cu = torch.zeros(4, dtype=torch.int32)
+    q, v = torch.empty(0, 2, 64, device="cuda"), torch.empty(0, 4, 32, device="cuda")
+    g = torch.empty(0, 4, device="cuda") if per_token else torch.full((4,), -0.1, device="cuda")
+    h0, dhT = torch.randn(3, 4, 64, 32, device="cuda"), torch.randn(3, 4, 64, 32, device="cuda")
+    kw = dict(cu_seqlens=cu.cuda(), cu_seqlens_cpu=cu)
+    out, hT = ck.linattn_fwd_chunked(q, q, v, g, h0, **kw)
+    assert out.shape == v.shape and torch.equal(hT, h0)
+    assert bool((ck.linattn_fwd_chunked(q, q, v, g, **kw)[1] == 0).all())
+    grads = ck.linattn_bwd_chunked(q, q, v, g, h0, v, dhT, **kw)
+    assert grads["dq"].shape == q.shape and torch.equal(grads["dh0"], dhT)
+    assert grads["dlog_decay"].shape == g.shape and bool((grads["dlog_decay"] == 0).all())
+
+
+def test_binding_refusals():
+    """Arguments that only a device can hold wrong."""
+    q, g = torch.zeros(1, 8, 2, 16, device="cuda"), torch.zeros(1, 8, 2, device="cuda")
+    cu = torch.tensor([0, 8], dtype=torch.int32)
+    for bad in (lambda: ck.linattn_fwd_chunked(q, q.transpose(1, 2).contiguous().transpose(1, 2), q, g),
+                lambda: ck.linattn_fwd_chunked(q, q.bfloat16(), q, g),
+                lambda: ck.linattn_fwd_chunked(q, q[:, :7].contiguous(), q, g),
+                lambda: ck.linattn_fwd_chunked(q, q, q, g.double()),
+                lambda: ck.linattn_fwd_chunked(q, q, q, g, cu_seqlens=cu.cuda(), cu_seqlens_cpu=cu.cuda()),
+                lambda: ck.linattn_fwd_chunked(q, q, q, g, cu_seqlens=cu.cuda() - 1),
+                lambda: ck.linattn_fwd_chunked(q, q, q, g, out=q),
+                lambda: ck.linattn_bwd_chunked(q, q, q, g, None, q.cpu()),
+                lambda: ck.linattn_decode_step(q[0], q[0], q[0], g[0], torch.zeros(8, 2, 16, 32, device="cuda")),
+                lambda: ck.block_norm(q, gate=q, gate_act="relu"),
+                lambda: ck.block_norm(q, gate=q),
+                lambda: ck.block_norm(q, post_group=48),
+                lambda: ck.block_norm(q, pre_weight=q[0, 0, 0])):
+        with pytest.raises((ValueError, TypeError, ck.CkdaError)):
+            bad()
+    torch.cuda.synchronize()
