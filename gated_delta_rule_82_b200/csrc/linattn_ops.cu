@@ -350,14 +350,20 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     if (!scan) v.fin = b.dh0;
     a.run[0] = q;
     a.run[1] = k;
-    a.runs = 2;
+    a.run[2] = v;
     // (the decay gradient is made of differences of q.dq and k.dk: they are formed in full
     // precision when it is asked for)
-    if ((e = launch_la_run(a, dv, dk, b.dg != nullptr, dtype, s)) != cudaSuccess) return e;
-    a.run[0] = v;
-    a.runs = 1;
-    a.after = 1;      // (nothing of it depends on the run before: they only follow each other)
-    if ((e = launch_la_run(a, dk, dv, false, dtype, s)) != cudaSuccess) return e;
+    const bool exact = b.dg != nullptr;
+    // Three runs of the same kernel go in one launch, side by side.
+    const bool one = dk == dv && (dtype == CKDA_F32 || (!exact && G == 1));
+    a.runs = one ? 3 : 2;
+    if ((e = launch_la_run(a, dv, dk, exact, dtype, s)) != cudaSuccess) return e;
+    if (!one) {
+        a.run[0] = v;
+        a.runs = 1;
+        a.after = 1;      // (nothing of it depends on the run before: they only follow each other)
+        if ((e = launch_la_run(a, dk, dv, false, dtype, s)) != cudaSuccess) return e;
+    }
 
     if (G > 1 && b.tokens > 0) {
         const long long vecs = b.tokens * (H / G) * (dk / 4);
