@@ -403,20 +403,28 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         if constexpr (!kSummary) la_wait_before();
         float2 st[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            st[j] = init ? make_float2(init[own + (size_t)(2 * j) * cs], init[own + (size_t)(2 * j + 1) * cs])
-                         : make_float2(0.f, 0.f);
-        if (fold) {                               // the units ahead of this one, in the run's order
-            const int ahead = rev ? min(u.count - 1 - u.index, a.sp.units - 1 - unit) : u.index;
+        for (int j = 0; j < 32; ++j) st[j] = make_float2(0.f, 0.f);
+        // the entering state, then (folded) the units ahead of this one, in the run's order.  Where a
+        // thread's channels lie one after the other it takes four at a time (a layer's backward with
+        // h0 and dhT: 176 us with single ones)
+        const int ahead = !fold ? 0 : rev ? min(u.count - 1 - u.index, a.sp.units - 1 - unit) : u.index;
 #pragma unroll 1
-            for (int k = 0; k < ahead; ++k) {
-                const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;
-                const float w = exp2f((float)R.unit_decay[un]);
-                const float* E = R.unit_state + un * (D * D) + own;
+        for (int k = init ? -1 : 0; k < ahead; ++k) {
+            const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;
+            const float w = k < 0 ? 0.f : exp2f((float)R.unit_decay[un]);
+            const float* E = (k < 0 ? init : R.unit_state + un * (D * D)) + own;
+            const float2 w2 = make_float2(w, w);
+            if (R.transposed) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float4 x = *reinterpret_cast<const float4*>(E + 4 * j);
+                    st[2 * j] = fma2(st[2 * j], w2, make_float2(x.x, x.y));
+                    st[2 * j + 1] = fma2(st[2 * j + 1], w2, make_float2(x.z, x.w));
+                }
+            } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    st[j] = fma2(st[j], make_float2(w, w),
-                                 make_float2(E[(size_t)(2 * j) * cs], E[(size_t)(2 * j + 1) * cs]));
+                    st[j] = fma2(st[j], w2, make_float2(E[(size_t)(2 * j) * D], E[(size_t)(2 * j + 1) * D]));
             }
         }
         bool ok = true;
@@ -629,12 +637,16 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 }
             }
             if (!kSummary && last && R.fin_dot) {
+                // (the run of dq, which holds its rows one channel after the other)
                 const float* f = R.fin_dot + seq_state + own;
-                double d = 0.0;
+                double d = 0.0, d2 = 0.0;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    d += (double)st[j].x * (double)f[(size_t)(2 * j) * cs] +
-                         (double)st[j].y * (double)f[(size_t)(2 * j + 1) * cs];
+                for (int j = 0; j < 16; ++j) {
+                    const float4 x = *reinterpret_cast<const float4*>(f + 4 * j);
+                    d += (double)st[2 * j].x * x.x + (double)st[2 * j].y * x.y;
+                    d2 += (double)st[2 * j + 1].x * x.z + (double)st[2 * j + 1].y * x.w;
+                }
+                d += d2;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
                 if (lane == 0) b.fin[warp - 8] = d;
