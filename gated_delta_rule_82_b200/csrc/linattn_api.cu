@@ -51,9 +51,16 @@ ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tok
     return CKDA_OK;
 }
 
-// Units that run side by side: a CTA per SM in the forward; in the backward, whose longest launch
-// holds two runs, half of that (4096 x 16 heads: 156 us; with 148 units, and two waves, 170 us).
-constexpr int kFwdSlots = 148, kBwdSlots = 74;
+// Units that run side by side.  On tcgen05 (bf16, 128 x 128) a CTA fills an SM; in the backward its
+// longest launch holds two runs (4096 x 16 heads: 156 us; with 148 units, and two waves, 170 us).
+// The warp tiles take a warp for 16 output channels: several narrow heads fit an SM, and a unit
+// leaves its SM waiting for longer than it takes to start another (4096 x 16 heads of 64 x 64:
+// forward 97 us with 148 units, 58 with 296; backward 405 with 74, 224 with 148, 192 with 296; fp32
+// backward of 128 x 128 806 with 74, 680 with 148).
+int unit_slots(int dk, int dv, ckda_dtype dtype, bool backward) {
+    if (dtype == CKDA_BF16 && dk == 128 && dv == 128) return backward ? 74 : 148;
+    return 148 * (128 / (dk > dv ? dk : dv));
+}
 
 LaSplit make_split(const Tokens& t, const int* cu, const int* cu_host, int H, int slots) {
     LaSplit sp;
@@ -87,8 +94,14 @@ size_t ckda_linattn_fwd_workspace_bytes(int B, int T, const int* cu_seqlens_host
     Tokens t;
     if (!supported_dim(dk) || !supported_dim(dv)) return (size_t)-1;
     if (read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t) != CKDA_OK) return (size_t)-1;
-    return la_fwd_workspace(make_split(t, nullptr, cu_seqlens_host, H, kFwdSlots), t.longest, dk,
-                            dv);
+    size_t need = 0;                    // of either type
+    for (ckda_dtype type : {CKDA_F32, CKDA_BF16}) {
+        const LaSplit sp =
+            make_split(t, nullptr, cu_seqlens_host, H, unit_slots(dk, dv, type, false));
+        const size_t n = la_fwd_workspace(sp, t.longest, dk, dv);
+        need = n > need ? n : need;
+    }
+    return need;
 }
 
 ckda_status ckda_linattn_fwd_chunked(const void* q, const void* k, const void* v,
@@ -112,7 +125,8 @@ ckda_status ckda_linattn_fwd_chunked(const void* q, const void* k, const void* v
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return CKDA_ERR_ALIGN;
     if (!aligned4(cu_seqlens) || !aligned4(log_decay)) return CKDA_ERR_ALIGN;
-    const LaSplit sp = make_split(t, cu_seqlens, cu_seqlens_host, H, kFwdSlots);
+    const LaSplit sp =
+        make_split(t, cu_seqlens, cu_seqlens_host, H, unit_slots(dk, dv, dtype, false));
     const size_t need = la_fwd_workspace(sp, t.longest, dk, dv);
     if (need > 0 && (!workspace || workspace_bytes < need)) return CKDA_ERR_WORKSPACE;
     const size_t es = elem_size(dtype), tok = (size_t)t.total, nst = (size_t)t.n * H * dk * dv * 4;
@@ -136,8 +150,15 @@ size_t ckda_linattn_bwd_workspace_bytes(int B, int T, const int* cu_seqlens_host
     if (!supported_dim(dk) || !supported_dim(dv)) return (size_t)-1;
     if (read_tokens(B, T, cu_seqlens_host, n_seqs, H, &t) != CKDA_OK) return (size_t)-1;
     if (qk_heads < 0 || (qk_heads > 0 && H % qk_heads != 0)) return (size_t)-1;
-    return la_bwd_workspace(make_split(t, nullptr, cu_seqlens_host, H, kBwdSlots), t.longest,
-                            t.total, qk_heads > 0 ? H / qk_heads : 1, dk, dv);
+    size_t need = 0;                    // of either type
+    for (ckda_dtype type : {CKDA_F32, CKDA_BF16}) {
+        const LaSplit sp =
+            make_split(t, nullptr, cu_seqlens_host, H, unit_slots(dk, dv, type, true));
+        const size_t n =
+            la_bwd_workspace(sp, t.longest, t.total, qk_heads > 0 ? H / qk_heads : 1, dk, dv);
+        need = n > need ? n : need;
+    }
+    return need;
 }
 
 ckda_status ckda_linattn_bwd_chunked(const void* q, const void* k, const void* v,
@@ -164,7 +185,8 @@ ckda_status ckda_linattn_bwd_chunked(const void* q, const void* k, const void* v
         if (p && !aligned16(p)) return CKDA_ERR_ALIGN;
     if (!aligned4(cu_seqlens) || !aligned4(log_decay) || !aligned4(dlog_decay))
         return CKDA_ERR_ALIGN;
-    const LaSplit sp = make_split(t, cu_seqlens, cu_seqlens_host, H, kBwdSlots);
+    const LaSplit sp =
+        make_split(t, cu_seqlens, cu_seqlens_host, H, unit_slots(dk_, dv_, dtype, true));
     const size_t need = la_bwd_workspace(sp, t.longest, t.total, G, dk_, dv_);
     if (!workspace || workspace_bytes < need) return CKDA_ERR_WORKSPACE;
     const size_t es = elem_size(dtype), tok = (size_t)t.total;

@@ -169,11 +169,14 @@ la_group_sum_kernel(const float* __restrict__ dqf, const float* __restrict__ dkf
 
 int la_unit_len(long long total, long long longest, int H, int slots) {
     const long long whole = (longest + kLaChunk - 1) / kLaChunk * kLaChunk;
+    // (two chunks in turn take less time than a launch of summaries: 100 tokens, forward 19.2 us a
+    // call against 23.9 in two units; 300 tokens, 31 against 24 in five)
+    if (whole <= 2 * kLaChunk) return (int)(whole < kLaChunk ? kLaChunk : whole);
     const int per = slots / H;          // units of all sequences that run side by side per head
-    if (per <= 1) return (int)(whole < kLaChunk ? kLaChunk : whole);
+    if (per <= 1) return (int)whole;
     long long L = ((total + per - 1) / per + kLaChunk - 1) / kLaChunk * kLaChunk;
-    if (L < 2 * kLaChunk) L = 2 * kLaChunk;
-    return (int)(L < whole ? L : whole < kLaChunk ? kLaChunk : whole);
+    if (L < kLaChunk) L = kLaChunk;
+    return (int)(L < whole ? L : whole);
 }
 
 long long la_units(const int* cu_host, int n, int T, int L) {
@@ -199,8 +202,8 @@ FwdWs fwd_ws(void* ws, bool split, long long units, int H, int dk, int dv) {
 }
 // more than one unit in a sequence; few enough for the runs to add the summaries up themselves
 bool is_split(const LaSplit& sp, long long longest) { return longest > sp.L; }
-bool is_folded(const LaSplit& sp, long long longest) {
-    return (longest + sp.L - 1) / sp.L <= kLaFoldUnits;
+bool is_folded(const LaSplit& sp, long long longest, int most) {
+    return (longest + sp.L - 1) / sp.L <= most;
 }
 }  // namespace
 
@@ -227,7 +230,7 @@ cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv,
     r.unit_state = w.states;
     r.unit_decay = w.decay;
     // (every unit reads h0 then, and the last one writes hT: not when they are the same)
-    r.fold = is_folded(f.sp, longest) && f.hT != f.h0;
+    r.fold = is_folded(f.sp, longest, kLaFoldUnits) && f.hT != f.h0;
     a.run[0] = r;
     cudaError_t e;
     if (f.sp.empty && f.hT && (!split || r.fold))
@@ -299,7 +302,11 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     rr.reverse = 1;
     rr.u_scale = b.scale;
     const bool want_dot = b.dg && b.dhT;
-    const bool fold = is_folded(sp, longest), scan = split && !fold;
+    // (the tcgen05 run of dq reads its summaries a thread a row, which a scan in coalesced reads beats
+    // from three units on: 256 tokens x 16 heads in four 52 -> 42 us; 2 x 2048 tokens in two units 147
+    // us, with a scan 151)
+    const bool tc = dtype == CKDA_BF16 && dk == 128 && dv == 128;
+    const bool fold = is_folded(sp, longest, tc ? 2 : kLaFoldUnits), scan = split && !fold;
     int parts = 1;
     if (sp.empty && b.dh0 && !scan) {
         a.run[0] = rr;
