@@ -34,8 +34,10 @@ LaRun blank_run() {
 // Sums in fp64: a gradient is a small difference of long sums.
 
 __global__ void __launch_bounds__(256)
-la_dg_suffix_kernel(LaSplit sp, const double* __restrict__ sq, double* __restrict__ sk,
-                    const double* __restrict__ dot, int parts) {
+la_dg_suffix_kernel(LaSplit sp, double* sq, double* __restrict__ sk,
+                    const double* __restrict__ dot, int parts, long long clear_to) {
+    la_let_next_start();
+    la_wait_before();
     const int w = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (w >= sp.n * sp.H) return;
     const int seq = w / sp.H, h = w - seq * sp.H;
@@ -47,6 +49,11 @@ la_dg_suffix_kernel(LaSplit sp, const double* __restrict__ sq, double* __restric
     }
     const int count = (len + kLaChunk - 1) / kLaChunk;
     const long long id0 = la_chunk_id(start, seq, 0);
+    if (clear_to) {       // numbers between this sequence's last chunk and the next one's first
+        const long long next = seq + 1 < sp.n ? la_chunk_id(start + len, seq + 1, 0) : clear_to;
+        for (long long id = id0 + count + lane; id < next && id < clear_to; id += 32)
+            sq[(size_t)id * sp.H + h] = 0.0;
+    }
     double behind = 0.0;
     if (dot)
         for (int p = 0; p < parts; ++p) behind += dot[(size_t)w * parts + p];
@@ -73,6 +80,8 @@ la_dg_rows_kernel(LaSplit sp, const float* __restrict__ g, int per_token,
                   const double* __restrict__ behind, float* __restrict__ dg,
                   double* __restrict__ sums) {
     __shared__ double part[8][32];
+    la_let_next_start();
+    la_wait_before();
     const UnitAt u = find_unit(sp, blockIdx.x);
     if (!u.ok) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -120,11 +129,12 @@ la_dg_rows_kernel(LaSplit sp, const float* __restrict__ g, int per_token,
     }
 }
 
-// Fixed decays: the sum over every chunk.  One CTA per head; chunk numbers that no chunk has are
-// zero (cleared before).
+// Fixed decays: the sum over every chunk.  One CTA per head; chunk numbers that no chunk has were
+// cleared by la_dg_suffix_kernel.
 __global__ void __launch_bounds__(256)
 la_dg_head_kernel(const double* __restrict__ sums, long long ids, int H, float* __restrict__ dg) {
     __shared__ double part[8];
+    la_wait_before();
     double s = 0.0;
     for (long long i = threadIdx.x; i < ids; i += 256) s += sums[(size_t)i * H + blockIdx.x];
 #pragma unroll
@@ -143,6 +153,8 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 la_group_sum_kernel(const float* __restrict__ dqf, const float* __restrict__ dkf, T* dq, T* dk,
                     long long vecs, int G, int dim) {
+    la_let_next_start();
+    la_wait_before();
     const float* src = blockIdx.y ? dkf : dqf;
     T* dst = blockIdx.y ? dk : dq;
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // four elements of the result
@@ -375,34 +387,29 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     if (G > 1 && b.tokens > 0) {
         const long long vecs = b.tokens * (H / G) * (dk / 4);
         const dim3 grid((unsigned)((vecs + 255) / 256), 2);
-        if (dtype == CKDA_BF16)
-            la_group_sum_kernel<<<grid, 256, 0, s>>>(w.dqf, w.dkf, (__nv_bfloat16*)b.dq,
-                                                     (__nv_bfloat16*)b.dk, vecs, G, dk);
-        else
-            la_group_sum_kernel<<<grid, 256, 0, s>>>(w.dqf, w.dkf, (float*)b.dq, (float*)b.dk, vecs,
-                                                     G, dk);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = dtype == CKDA_BF16
+                ? la_launch_after(la_group_sum_kernel<__nv_bfloat16>, grid, 256, 0, s, w.dqf, w.dkf,
+                                  (__nv_bfloat16*)b.dq, (__nv_bfloat16*)b.dk, vecs, G, dk)
+                : la_launch_after(la_group_sum_kernel<float>, grid, 256, 0, s, w.dqf, w.dkf,
+                                  (float*)b.dq, (float*)b.dk, vecs, G, dk);
+        if (e != cudaSuccess) return e;
     }
     if (b.dg) {
         const long long ids = (long long)la_chunk_ids(b.tokens, sp.n);
-        la_dg_suffix_kernel<<<(sp.n * H + 7) / 8, 256, 0, s>>>(sp, w.sq, w.sk,
-                                                                want_dot ? w.dot : nullptr, parts);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        e = la_launch_after(la_dg_suffix_kernel, dim3((unsigned)((sp.n * H + 7) / 8)), 256, 0, s, sp,
+                            w.sq, w.sk, want_dot ? w.dot : nullptr, parts, b.per_token ? 0ll : ids);
+        if (e != cudaSuccess) return e;
         // (w.sq has been read: it takes the chunks' sums of a fixed decay's gradient)
-        if (!b.per_token &&
-            (e = cudaMemsetAsync(w.sq, 0, (size_t)ids * H * sizeof(double), s)) != cudaSuccess)
-            return e;
         LaSplit rows = sp;
         rows.L = kLaChunk;
         rows.units = b.chunks;
-        if (rows.units > 0)
-            la_dg_rows_kernel<<<rows.units, 256, 0, s>>>(rows, b.g, b.per_token, w.rq, w.rk, w.sk,
-                                                         b.dg, w.sq);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if (!b.per_token) {
-            la_dg_head_kernel<<<H, 256, 0, s>>>(w.sq, ids, H, b.dg);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        }
+        if (rows.units > 0 &&
+            (e = la_launch_after(la_dg_rows_kernel, dim3((unsigned)rows.units), 256, 0, s, rows, b.g,
+                                 b.per_token, w.rq, w.rk, w.sk, b.dg, w.sq)) != cudaSuccess)
+            return e;
+        if (!b.per_token && (e = la_launch_after(la_dg_head_kernel, dim3((unsigned)H), 256, 0, s, w.sq,
+                                                 ids, H, b.dg)) != cudaSuccess)
+            return e;
     }
     return cudaSuccess;
 }

@@ -23,7 +23,7 @@
 // What bounds it: the element work of a chunk, about 3100 cycles in the state warps (read U, decay,
 // write the state as an operand, outputs to memory) where HBM alone would allow 2700; tensor pipe 31 %
 // busy, 0.5 instructions a cycle and scheduler.  16 heads: 2 x 2048 tokens, run 20 us and summary 16 of
-// the forward's 38.6 a call; 65536 tokens, run 202 (4.0 TB/s of its own bytes) and summary 125 of 375.
+// the forward's 38.6 a call; 65536 tokens, run 202 (5.3 TB/s of its own bytes) and summary 125 of 375.
 // Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
 // once its copies and products have landed.
 #include <cuda.h>
