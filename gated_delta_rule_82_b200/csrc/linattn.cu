@@ -25,7 +25,7 @@
 // What bounds it: latency.  A warp holds a state and its operands in 200 registers, so an SM has 8 to
 // 12 warps, 0.27 instructions a cycle and scheduler, the mma.sync pipe 20 to 30 % busy; an fp32 chunk
 // takes six products of terms for one.  16 heads x 4096 tokens: bf16 64 x 64 forward 58 us, backward
-// 192; fp32 128 x 128 forward 224 us, backward 683; fp32 3 x 333 tokens x 6 heads backward 59 us.
+// 192; fp32 128 x 128 forward 237 us, backward 704; fp32 3 x 333 tokens x 6 heads backward 51 us.
 #include "linattn.cuh"
 
 namespace ckda {
@@ -182,7 +182,9 @@ struct Fetch {
 
 // acc += A B for the leading terms, low += A B for the other pairs whose product is not below the
 // precision kept.  Two accumulators, because the tensor core's sums do not round to nearest: what
-// is lost then is a part of the few leading products only.
+// is lost then is a part of the few leading products only.  With three terms those are added in fp32
+// one tile at a time, so that no loss carries on (errors of fp32 results 2.0e-7 -> 1.2e-7, about half the
+// plain fp32 form's; 4096 x 16 heads 128 x 128 forward 224 -> 237 us, 64 x 64 backward 276 -> 281).
 template <int NA, int NB>
 __device__ __forceinline__ void mma_terms(float acc[4], float low[4], const uint32_t (*a)[4],
                                           const uint32_t (*b)[2]) {
@@ -194,7 +196,14 @@ __device__ __forceinline__ void mma_terms(float acc[4], float low[4], const uint
             const int j = s - i;
             if (j >= 0 && j < NB) mma(low, a[i], b[j][0], b[j][1]);
         }
-    mma(acc, a[0], b[0][0], b[0][1]);
+    if constexpr (N == 3) {
+        float f[4] = {};
+        mma(f, a[0], b[0][0], b[0][1]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += f[k];
+    } else {
+        mma(acc, a[0], b[0][0], b[0][1]);
+    }
 }
 
 template <typename T, int DC, int DO, bool kSummary, int NP>
