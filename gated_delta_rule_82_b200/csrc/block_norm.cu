@@ -20,6 +20,7 @@
 // by the latency of loads and sums (4 channels a thread 66 us; three CTAs an SM, with spills, 89).
 #include "common.cuh"
 #include "block_norm.cuh"
+#include "linattn.cuh"        // la_launch_after
 
 namespace ckda {
 
@@ -320,6 +321,7 @@ block_norm_kernel(const BlockNormArgs p) {
 template <typename T, int TPR, bool kVec, int kAct>
 __global__ void __launch_bounds__(threads_of<TPR>(), bwd_ctas<TPR>())
 block_norm_bwd_kernel(const BlockNormArgs p, const BlockNormGrads g) {
+    la_let_next_start();
     constexpr int THREADS = threads_of<TPR>(), RPC = THREADS / TPR;
     extern __shared__ __align__(16) float sw[];
     __shared__ float2 slots[2 * THREADS / 32];
@@ -471,6 +473,7 @@ struct ReduceArgs {
 };
 __global__ void __launch_bounds__(1024)
 block_norm_reduce_kernel(const ReduceArgs a) {
+    la_wait_before();
     __shared__ float part[32][33];
     const int k = blockIdx.y, cols = a.cols[k];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
@@ -614,8 +617,8 @@ cudaError_t launch_block_norm_bwd(const BlockNormArgs& p, const BlockNormGrads& 
     add(g.dw_pre, p.D);
     add(g.dr, p.D);
     if (k == 0) return cudaSuccess;
-    block_norm_reduce_kernel<<<dim3((widest + 31) / 32, k), 1024, 0, s>>>(r);
-    return cudaGetLastError();
+    // (it starts as the backward's CTAs leave; before that they fill the SMs)
+    return la_launch_after(block_norm_reduce_kernel, dim3((widest + 31) / 32, k), 1024, 0, s, r);
 }
 
 }  // namespace ckda
