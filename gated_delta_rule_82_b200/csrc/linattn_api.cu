@@ -52,7 +52,8 @@ ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tok
 }
 
 // Units that run side by side.  On tcgen05 (bf16, 128 x 128) a CTA fills an SM; in the backward its
-// longest launch holds two runs (4096 x 16 heads: 156 us; with 148 units, and two waves, 170 us).
+// longest launch holds two runs (16 heads, 2 x 2048 tokens: 144 us, with 100 units 174, with 148 146;
+// 2 x 1000 tokens: 92, 107, 96).
 // The warp tiles take a warp for 16 output channels: several narrow heads fit an SM, and a unit
 // leaves its SM waiting for longer than it takes to start another (4096 x 16 heads of 64 x 64:
 // forward 97 us with 148 units, 58 with 296; backward 405 with 74, 224 with 148, 192 with 296; fp32
