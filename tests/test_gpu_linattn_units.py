@@ -84,3 +84,44 @@ def test_fixed_decays_over_packed_gaps():
     want, big = ref.backward(*args, cu)
     got = ck.linattn_bwd_chunked(*args, cu_seqlens=cu.cuda(), cu_seqlens_cpu=cu, workspace=ws)
     _check(got, want, big, max(lens) + 128)
+
+
+def _same(a, b, steps):
+    """bf16 values that differ by rounding only: `steps` times 2^-8 of the largest."""
+    return float((a.float() - b.float()).abs().max()) <= steps * 2 ** -8 * float(b.float().abs().max())
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in an array: the last tokens, rows and sequences are those of a call on
+    the tail alone (decays of e^-0.05 a token on average forget what lies 3000 tokens back)."""
+    torch.cuda.empty_cache()
+    T, H, d, tail = 1_060_001, 16, 128, 5000
+    rand = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_().mul_(s[-1] ** -0.5)
+    q, k, v, do = (rand(1, T, H, d) for _ in range(4))
+    g = -0.1 * torch.rand(1, T, H, device="cuda")
+    part = [x[:, -tail - 3000:].contiguous() for x in (q, k, v, g)]
+    out, hT = ck.linattn_fwd_chunked(q, k, v, g)
+    o2, h2 = ck.linattn_fwd_chunked(*part)
+    assert _same(out[:, -tail:], o2[:, 3000:], 2) and float((hT - h2).abs().max()) < 1e-5
+    grads = ck.linattn_bwd_chunked(q, k, v, g, None, do)
+    less = ck.linattn_bwd_chunked(*part, None, do[:, -tail - 3000:].contiguous())
+    for n in ("dq", "dk", "dv", "dlog_decay"):
+        assert _same(grads[n][:, -tail:], less[n][:, 3000:], 2), n
+    del grads, out, do
+    rows = q.view(-1, 2048), k.view(-1, 2048), v.view(-1, 2048)
+    kw = dict(gate_act="silu", post_group=2048, pre_norm=True)
+    h, n = ck.block_norm(rows[0], gate=rows[1], residual=rows[2], **kw)
+    last = [r[-9:].contiguous() for r in rows]
+    h2, n2 = ck.block_norm(last[0], gate=last[1], residual=last[2], **kw)
+    assert torch.equal(h[-9:], h2) and torch.equal(n[-9:], n2)
+    del h, n, q, k, v, rows
+    N = 4200
+    state = torch.empty(N, 32, 128, 128, device="cuda").normal_()
+    q, k, v = (rand(N, 32, 128) for _ in range(3))
+    g = -torch.rand(N, 32, device="cuda")
+    end = state[-3:].clone()
+    o = ck.linattn_decode_step(q, k, v, g, state)
+    o2 = ck.linattn_decode_step(*(x[-3:].contiguous() for x in (q, k, v, g)), end)
+    assert torch.equal(o[-3:], o2) and torch.equal(state[-3:], end)
+    del state
+    torch.cuda.empty_cache()
