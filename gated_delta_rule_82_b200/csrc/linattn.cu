@@ -17,10 +17,9 @@
 // Precision: every value enters the products as a sum of bf16 terms: one for a bf16 input
 // (exact), three for an fp32 one (8 bits each, 24 in all; the products of terms below 2^-24 are
 // left out).  The weighted z of the state update always has three, so states are fp32-grade
-// whatever the input type; P and M as operands have three when `exact` asks for it, else P two and M
-// one: of the operands of a bf16 output only the state is rounded to bf16.  (With one term of P too,
-// outputs that are small differences of the chunk's own part and the state's had 1.6 times the error
-// of their own rounding.)
+// whatever the input type; P and M as operands have three when `exact` asks for it, else two, which
+// leave 2^-16 of a product, far below a bf16 output's own rounding.  (With one term of M outputs were
+// 1.24 times as far off as their rounding, with one of P too 1.6 times.)
 //
 // What bounds it: latency.  A warp holds a state and its operands in 200 registers, so an SM has 8 to
 // 12 warps, 0.27 instructions a cycle and scheduler, the mma.sync pipe 20 to 30 % busy; an fp32 chunk
@@ -87,8 +86,7 @@ struct RunShape {
     static constexpr int LC = DC + 8, LO = DO + 8, LP = C + 8;   // row pitches: 16 bytes of padding
     static constexpr int XY = C * LC, Z = C * LO;      // (elements; keeps ldmatrix conflict-free)
     static constexpr int STAGE = NI * (XY * (kSummary ? 1 : 2) + Z);
-    static constexpr int PT = NP == 1 ? 2 : NP;        // terms of P
-    static constexpr int PP = kSummary ? 0 : PT * C * LP;
+    static constexpr int PP = kSummary ? 0 : NP * C * LP;
     static constexpr size_t SMEM = (size_t)(STAGES * STAGE + PP) * 2 + 2 * (4 * C + 8) * 4 +
                                    (kSummary ? 0 : NW * C * 4);
 };
@@ -210,7 +208,7 @@ template <typename T, int DC, int DO, bool kSummary, int NP>
 __global__ void __launch_bounds__(DO * 2)
 la_run_kernel(const LaArgs a) {
     using S = RunShape<T, DC, DO, kSummary, NP>;
-    constexpr int NW = S::NW, NI = S::NI, LC = S::LC, LO = S::LO, LP = S::LP, PT = S::PT;
+    constexpr int NW = S::NW, NI = S::NI, LC = S::LC, LO = S::LO, LP = S::LP;
     constexpr int KC = DC / 16;                 // 16-deep steps over the contracted channels
     constexpr int NU = 3;                       // terms of the weighted z
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -388,10 +386,10 @@ la_run_kernel(const LaArgs a) {
                             const bool keep = rev ? row <= col + e : row >= col + e;
                             w[e] = keep ? (p[n][2 * e2 + e] + pl[n][2 * e2 + e]) * exp2f(rev ? -d : d) * R.p_scale : 0.f;
                         }
-                        uint32_t t3[PT];
-                        split2<PT>(w[0], w[1], t3);
+                        uint32_t t3[NP];
+                        split2<NP>(w[0], w[1], t3);
 #pragma unroll
-                        for (int q = 0; q < PT; ++q)
+                        for (int q = 0; q < NP; ++q)
                             *reinterpret_cast<uint32_t*>(sP + q * C * LP + row * LP + col) = t3[q];
                     }
             }
@@ -454,13 +452,13 @@ la_run_kernel(const LaArgs a) {
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                     if (rev ? m > kk : m < kk) continue;
-                    uint32_t fp[PT][4];
+                    uint32_t fp[NP][4];
 #pragma unroll
-                    for (int q = 0; q < PT; ++q)
+                    for (int q = 0; q < NP; ++q)
                         ldsm4(fp[q], smem_addr(sP + q * C * LP + (m * 16 + (lane & 15)) * LP +
                                                kk * 16 + (lane >> 4) * 8));
-                    mma_terms<PT, NI>(acc[m][0], low[m][0], fp, b[0]);
-                    mma_terms<PT, NI>(acc[m][1], low[m][1], fp, b[1]);
+                    mma_terms<NP, NI>(acc[m][0], low[m][0], fp, b[0]);
+                    mma_terms<NP, NI>(acc[m][1], low[m][1], fp, b[1]);
                 }
             }
         }
@@ -703,9 +701,9 @@ cudaError_t launch_t(const LaArgs& a, cudaStream_t s) {
 
 template <typename T, int DC, int DO>
 cudaError_t launch_do(const LaArgs& a, bool summary, bool exact, cudaStream_t s) {
-    if (summary) return launch_t<T, DC, DO, true, 1>(a, s);
+    if (summary) return launch_t<T, DC, DO, true, 2>(a, s);
     if constexpr (sizeof(T) == 2)
-        if (!exact) return launch_t<T, DC, DO, false, 1>(a, s);
+        if (!exact) return launch_t<T, DC, DO, false, 2>(a, s);
     return launch_t<T, DC, DO, false, 3>(a, s);
 }
 

@@ -10,20 +10,21 @@
 // X, Y, Z arrive by TMA as 128-byte-swizzled tiles; one tile serves as K-major and as MN-major
 // operand.  The state lives in the registers of eight warps (a row of 64 channels per thread) and
 // goes to the tensor core as a bf16 operand through TMEM; the weighted Z as well, in three bf16
-// terms (24 bits, 32 columns each), so that states are fp32-grade.  P has two terms, so that of the
-// operands only the state is rounded to bf16 (the output's own rounding comes on top).  With NP = 3 the
-// scores and the state enter in three terms too (the state's second and third from shared memory).
+// terms (24 bits, 32 columns each), so that states are fp32-grade.  P and the state have NP terms where
+// they are read: two leave 2^-16 of a product, far below an output's own rounding to bf16 (one term of
+// the state, the output's own precision, made outputs 1.24 times as far off); three are fp32-grade.
+// The state's lower terms lie in shared memory, half of the second one at NP = 2 in TMEM's last columns.
 //
 // Roles (one CTA per SM, all of TMEM): warps 0-7 weight Z; 8-15 carry the state and write the
 // outputs; 16-19 turn scores into P; then one warp each for the decays, the products U, Sc (and
 // TMA), and O1 with O2 (a poll of a barrier takes 80 cycles even when it is complete, so one warp
 // that issued all of them would be the slowest part).  They meet on mbarriers only, so a chunk's
 // products overlap the neighbours' element work: per chunk the tensor pipe needs 256 (Sc) + 768 (U)
-// + 256 (O1) + 400 (O2) cycles at NP = 1.
-// What bounds it: the element work of a chunk, about 3100 cycles in the state warps (read U, decay,
-// write the state as an operand, outputs to memory) where HBM alone would allow 2700; tensor pipe 31 %
-// busy, 0.5 instructions a cycle and scheduler.  16 heads: 2 x 2048 tokens, run 20 us and summary 16 of
-// the forward's 38.6 a call; 65536 tokens, run 202 (5.3 TB/s of its own bytes) and summary 125 of 375.
+// + 530 (O1) + 400 (O2) cycles at NP = 2.
+// What bounds it: the element work of a chunk, about 3700 cycles in the state warps (read U, decay,
+// write the state as an operand, outputs to memory) where HBM alone would allow 2700.  16 heads: 2 x
+// 2048 tokens, forward 42.9 us a call (with one term of the state 38.7), 65536 tokens 400 (359), the
+// summary's launch 16 and 125 of them.
 // Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
 // once its copies and products have landed.
 #include <cuda.h>
@@ -46,7 +47,7 @@ constexpr int kGateRing = 4;
 constexpr int kPolls = 1 << 20;
 
 // TMEM columns
-constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320;
+constexpr uint32_t kColU = 0, kColS = 128, kColO1 = 192, kColO2 = 256, kColSc = 320, kColSlo = 480;
 
 __device__ int g_la_status;               // 0, or kLaStatusWait since the host last read it
 
@@ -78,16 +79,14 @@ struct Ring {
 
 template <int NP, bool kSummary>
 struct TcShape {
-    static constexpr int STAGES = kSummary ? 4 : NP == 1 ? 3 : 2;
+    static constexpr int STAGES = kSummary ? 4 : NP == 2 ? 3 : 2;
     static constexpr int STAGE = kSummary ? 2 * kTile : 3 * kTile;       // Y, Z, X
-    static constexpr int PBUF = NP == 1 ? 2 : 1;                         // buffers of P
-    static constexpr int PT = NP == 1 ? 2 : NP;                          // terms of P
-    static constexpr int P = kSummary ? 0 : PBUF * PT * kBlock;
+    static constexpr int P = kSummary ? 0 : NP * kBlock;
     static constexpr int OUT = kSummary ? 0 : 2 * kTile;                 // outputs on their way out
-    static constexpr int SLO = kSummary ? 0 : (NP - 1) * D * D * 2;      // lower terms of the state
+    static constexpr int SLO = kSummary ? 0 : NP == 2 ? D * D : (NP - 1) * D * D * 2;  // lower terms of the state
     static constexpr int GATES = STAGES * STAGE + P + SLO + OUT;
     static constexpr int DOT = GATES + kGateRing * (int)sizeof(GateSlot);
-    static constexpr int BARS = DOT + (NP > 1 ? kGateRing * 4 * C * 4 : 0);
+    static constexpr int BARS = DOT + (NP == 3 ? kGateRing * 4 * C * 4 : 0);
     static constexpr int SMEM = BARS + 512 + 1024;                       // (+ alignment of the base)
     static constexpr int EXTRA = kSummary ? 16 : 20;                     // first of the single warps
     static constexpr int THREADS = (EXTRA + (kSummary ? 3 : 4)) * 32;
@@ -97,7 +96,7 @@ struct TcShape {
 
 struct Bars {
     uint64_t full[4], empty[4], gfull[kGateRing], gempty[kGateRing];
-    uint64_t sc_full, sc_empty, p_full[2], p_empty[2], wz_full[2], wz_empty[2];
+    uint64_t sc_full, sc_empty, p_full, p_empty, wz_full[2], wz_empty[2];
     uint64_t u_full[2], u_empty[2], s_full, s_empty, o_full, o_empty, dot_full[kGateRing], dot_empty[kGateRing], fin_full, tail, drain[3];
     double fin[8];
     uint32_t tmem;
@@ -137,6 +136,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {   // a in the low 
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The thread's number, read anew: what is derived from it is formed where it is used and holds no
+// register over the chunks (the state's warps have none to spare).
+__device__ __forceinline__ int thread_again() {
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    return t;
+}
 
 // Registers per thread of this warpgroup (all four warps).  A run launches with 80 (24 warps); the
 // shares below add up to 6 x 80, so every raise finds what the others gave back.
@@ -202,7 +209,11 @@ __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t* v)
         "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15]) : "memory");
 }
-// 32 lanes x 8 columns, a lane per thread.
+// 32 lanes x 4 or 8 columns, a lane per thread.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                  ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
@@ -256,6 +267,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t r[4], uint32_t a) {
 __device__ __forceinline__ void stsm4t(uint32_t a, const uint32_t r[4]) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
                  :: "r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+// 16-byte piece of a 128-byte row of a swizzled tile; row: the address of its piece 0.  (Formed at the
+// store: addresses held over the loop cost more registers than the state's warps have.)
+__device__ __forceinline__ void st_piece(uint32_t row, uint32_t piece, const uint32_t v[4]) {
+    asm volatile("{\n\t.reg .b32 a;\n\txor.b32 a, %0, %1;\n\tst.shared.v4.b32 [a], {%2, %3, %4, %5};\n\t}"
+                 ::"r"(row), "r"(piece << 4), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 // The output warps' staging: 32 tokens x 32 channels of bf16 per warp, 16-byte pieces swizzled so
 // that eight neighbouring tokens lie in different banks.
@@ -311,9 +328,9 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&b.wz_full[i], 8);
             tc::mbar_init(&b.wz_empty[i], 1);
-            tc::mbar_init(&b.p_full[i], 4);
-            tc::mbar_init(&b.p_empty[i], 1);
         }
+        tc::mbar_init(&b.p_full, 4);
+        tc::mbar_init(&b.p_empty, 1);
         tc::mbar_init(&b.sc_full, 1);
         tc::mbar_init(&b.sc_empty, 4);
         for (int i = 0; i < 2; ++i) {
@@ -432,15 +449,34 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
         }
         bool ok = true;
+        auto again = [&]() { return NP == 2 ? thread_again() : tid; };
         auto put_state = [&](int i) {             // the state entering chunk i, as an operand
+            const int tid = again(), lane = tid & 31, quarter = (tid >> 5) & 3, half = (tid >> 7) & 1;
+            const int row = 32 * quarter + lane;
+            // this row of its lower terms (NP = 2: channels 64-127 only)
+            const uint32_t slo = tc::smem_u32(sSlo) + (NP == 3 ? half * (D * 128) : 0) + row * 128 + ((row & 7) << 4);
             if (i > 0 && !wait(b, &b.s_empty, (i - 1) & 1)) return false;
             tc::tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint32_t t[8];
-                if constexpr (NP == 1) {
+                if constexpr (NP == 2) {
+                    // the second term: of channels 0-63 through TMEM too, of the others through shared memory
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) t[j] = pack2(st[8 * k + j].x, st[8 * k + j].y);
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t m[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = st[8 * k + 4 * q + j];
+                            const uint32_t hi = pack2(x.x, x.y);
+                            m[j] = pack2(x.x - lo_f(hi), x.y - hi_f(hi));
+                            t[4 * q + j] = hi;
+                        }
+                        if (half == 0)
+                            tmem_st4(tc::tmem_addr(tmem, 32 * quarter, kColSlo + 8 * k + 4 * q), m);
+                        else
+                            st_piece(slo, 2 * k + q, m);
+                    }
                 } else {
                     // three terms: the first through TMEM, the others through shared memory
 #pragma unroll
@@ -453,32 +489,28 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                             m[j] = cut2(x);
                             l[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
                         }
-                        uint8_t* at = sSlo + half * (D * 128) + row * 128 + (((2 * k + q) ^ (row & 7)) << 4);
-                        *reinterpret_cast<uint4*>(at) = make_uint4(m[0], m[1], m[2], m[3]);
-                        *reinterpret_cast<uint4*>(at + D * D * 2) = make_uint4(l[0], l[1], l[2], l[3]);
+                        st_piece(slo, 2 * k + q, m);
+                        st_piece(slo + D * D * 2, 2 * k + q, l);
                     }
                 }
                 tmem_st8(tc::tmem_addr(tmem, 32 * quarter, kColS + 32 * half + 8 * k), t);
             }
             tc::tmem_st_wait();
-            if constexpr (NP > 1) tc::fence_proxy_async_smem();
+            if (NP == 3 || half == 1) tc::fence_proxy_async_smem();
             tc::tc_fence_before();
             arrive_warp(&b.s_full);
             return true;
         };
-        // Outputs: this warp's 32 channels, 32 of the chunk's tokens
-        const int gr = lane >> 2, gc = 2 * (lane & 3);
-        const int ch0 = 32 * quarter, tq = 32 * half;
-        const int tr = lane >> 2, tp = lane & 3;                 // row and 16-byte piece, 8 rows a time
-        const int m4 = lane >> 3;                                // matrix of an x4 access
-        uint8_t* sOut0 = sSlo + S::SLO + (warp - 8) * (kTile / 8);      // two areas, a tile apart
         constexpr bool dots = kDots;
         // The rows that the outputs are multiplied with, into the staging area, long before their use.
         auto fetch_rows = [&](int i) {
+            const int tid = again(), warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+            const int ch0 = 32 * quarter, tq = 32 * ((warp >> 2) & 1);
+            const int tr = lane >> 2, tp = lane & 3;             // row and 16-byte piece, 8 rows a time
             const int Hd = H / R.dg, live = live_of(i) - tq;
             const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(R.dot) +
                                        ((size_t)(u.tok + chunk_at(i) * C + tq) * Hd + h / R.dg) * D + ch0 + 8 * tp;
-            uint8_t* sOut = sOut0 + (i & 1) * kTile;
+            uint8_t* sOut = sSlo + S::SLO + (warp - 8) * (kTile / 8) + (i & 1) * kTile;
             if (lane == 0) tc::bulk_wait_read<1>();              // (what was last stored from it)
             __syncwarp();
 #pragma unroll
@@ -490,10 +522,16 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        // Outputs: this warp's 32 channels, 32 of the chunk's tokens; two staging areas, a tile apart
         auto put_out = [&](int i) {
+            const int tid = again(), warp = tid >> 5, lane = tid & 31, quarter = warp & 3;
+            const int ch0 = 32 * quarter, tq = 32 * ((warp >> 2) & 1);
+            const int tr = lane >> 2, tp = lane & 3;             // row and 16-byte piece, 8 rows a time
+            const int gr = lane >> 2, gc = 2 * (lane & 3);
+            const int m4 = lane >> 3;                            // matrix of an x4 access
             const int gs = i % kGateRing, c = chunk_at(i), live = live_of(i) - tq;
             const long long tok = u.tok + (long long)c * C + tq;
-            uint8_t* sOut = sOut0 + (i & 1) * kTile;
+            uint8_t* sOut = sSlo + S::SLO + (warp - 8) * (kTile / 8) + (i & 1) * kTile;
             if constexpr (dots) {
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             } else if (lane == 0) {
@@ -664,11 +702,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         }
     } else if (!kSummary && warp < S::EXTRA) {
         // -------------------------------------------------------------------- P from the scores
-        constexpr int PB = S::PBUF, PT = S::PT;
         const int gr = lane >> 2, gc = 2 * (lane & 3);
         const float p_scale = R.p_scale;
         // P is zero beyond the diagonal: those 16 x 8 tiles are cleared once and stay
-        for (int k = 0; k < PB * PT; ++k)
+        for (int k = 0; k < NP; ++k)
             for (int w = lane; w < 16 * 8; w += 32) {
                 const int row = 16 * quarter + (w >> 3), c8 = w & 7;
                 if (rev ? c8 < 2 * quarter : c8 > 2 * quarter + 1)
@@ -683,13 +720,13 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int q = 0; q < PT; ++q)       // (two terms: the second rounds what is left)
+                    for (int q = 0; q < NP; ++q)       // (two terms: the second rounds what is left)
                         *reinterpret_cast<uint32_t*>(p + q * kBlock + e * 1024 + at) =
-                            PT == 2 && q == 1 ? pack2(w[2 * j + e].x, w[2 * j + e].y) : cut2(w[2 * j + e]);
+                            NP == 2 && q == 1 ? pack2(w[2 * j + e].x, w[2 * j + e].y) : cut2(w[2 * j + e]);
             }
         };
         auto make_p = [&](int i) {
-            const int gs = i % kGateRing, buf = i % PB;
+            const int gs = i % kGateRing;
             if (!wait(b, &b.gfull[gs], (i / kGateRing) & 1)) return false;
             const GateSlot& g = gates[gs];
             const int r0 = 16 * quarter + gr;
@@ -703,10 +740,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             const float rl[2] = {g.l[r0], g.l[r0 + 8]};
             const float sg = rev ? -1.f : 1.f;
             if (!wait(b, &b.sc_full, i & 1)) return false;
-            if (i >= PB && !wait(b, &b.p_empty[buf], (i / PB - 1) & 1)) return false;
+            if (i > 0 && !wait(b, &b.p_empty, (i - 1) & 1)) return false;
             tc::tc_fence_after();
             const uint32_t sc = tc::tmem_addr(tmem, 32 * quarter, kColSc);
-            uint8_t* p = sP + buf * PT * kBlock + r0 * 128 + gc * 2;
+            uint8_t* p = sP + r0 * 128 + gc * 2;
             float2 x[4], nx[4];
             tmem_ld_16x16(sc + 16 * quarter, x);
             // the diagonal tile, while the first of the others is on its way (outwards from it)
@@ -750,7 +787,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             arrive_warp(&b.sc_empty);
             arrive_warp(&b.gempty[gs]);
             tc::fence_proxy_async_smem();
-            arrive_warp(&b.p_full[buf]);
+            arrive_warp(&b.p_full);
             return true;
         };
         for (int i = 0; i < n; ++i)
@@ -964,7 +1001,6 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             constexpr uint32_t id_o2 = tc::idesc_bf16_f32(128, 64, 1, 0);
             const uint64_t xd0 = tc::smem_desc_sw128(tc::smem_u32(sm) + 2 * kTile, 16, 1024);
             const uint64_t zd0 = tc::smem_desc_sw128(tc::smem_u32(sm) + kTile, kBlock, 1024);
-            Ring<S::PBUF> pb;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 if (!(ok = tiles(i))) break;
@@ -974,7 +1010,17 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 tc::tc_fence_after();
                 const uint64_t xd = tc::desc_add(xd0, at.slot * S::STAGE);
                 if (elect_one()) {
-                    if constexpr (NP > 1) {
+                    if constexpr (NP == 2) {
+                        const uint64_t sd = tc::smem_desc_sw128(tc::smem_u32(sSlo), 16, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_tmem_a(tmem + kColO1, tmem + kColSlo + 8 * ks, tc::desc_add(xd, ks * 32),
+                                       id_o1, ks > 0);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma_bf16(tmem + kColO1, tc::desc_add(sd, ks * 32),
+                                         tc::desc_add(xd, kBlock + ks * 32), id_o1, 1);
+                    } else {
 #pragma unroll 1
                         for (int q = NP - 2; q >= 0; --q) {
                             const uint64_t sd =
@@ -990,31 +1036,29 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         mma_tmem_a(tmem + kColO1, tmem + kColS + 8 * ks,
-                                   tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1,
-                                   NP > 1 || ks > 0);
+                                   tc::desc_add(xd, (ks >> 2) * kBlock + (ks & 3) * 32), id_o1, 1);
                     tc::mma_commit(&b.s_empty);
                 }
                 __syncwarp();
                 // O2: the chunk's own scores
-                if (!(ok = wait(b, &b.p_full[pb.slot], pb.phase))) break;
+                if (!(ok = wait(b, &b.p_full, i & 1))) break;
                 tc::tc_fence_after();
                 const uint64_t zd = tc::desc_add(zd0, at.slot * S::STAGE);
                 if (elect_one()) {
 #pragma unroll 1
-                    for (int q = S::PT - 1; q >= 0; --q) {
+                    for (int q = NP - 1; q >= 0; --q) {
                         const uint64_t pd =
-                            tc::smem_desc_sw128(tc::smem_u32(sP) + (pb.slot * S::PT + q) * kBlock, 16, 1024);
+                            tc::smem_desc_sw128(tc::smem_u32(sP) + q * kBlock, 16, 1024);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
                             tc::mma_bf16(tmem + kColO2, tc::desc_add(zd, ks * 2048),
-                                         tc::desc_add(pd, ks * 32), id_o2, q < S::PT - 1 || ks > 0);
+                                         tc::desc_add(pd, ks * 32), id_o2, q < NP - 1 || ks > 0);
                     }
-                    tc::mma_commit(&b.p_empty[pb.slot]);
+                    tc::mma_commit(&b.p_empty);
                     tc::mma_commit(&b.o_full);
                     tc::mma_commit(&b.empty[at.slot]);
                 }
                 __syncwarp();
-                pb.next();
                 at.next();
             }
         }
@@ -1098,14 +1142,14 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s) {
-    return launch<1, true, false, false>(a, s);
+    return launch<2, true, false, false>(a, s);
 }
 // (the runs of one launch agree in out_f32 and in having rows to multiply with; the latter are exact)
 cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s) {
     const bool f32 = a.run[0].out_f32, dots = a.run[0].dot != nullptr;
     if (dots) return f32 ? launch<3, false, true, true>(a, s) : launch<3, false, false, true>(a, s);
     if (exact) return f32 ? launch<3, false, true, false>(a, s) : launch<3, false, false, false>(a, s);
-    return f32 ? launch<1, false, true, false>(a, s) : launch<1, false, false, false>(a, s);
+    return f32 ? launch<2, false, true, false>(a, s) : launch<2, false, false, false>(a, s);
 }
 
 // Read this file's status word (`stream` has finished) and clear it.

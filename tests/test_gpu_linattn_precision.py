@@ -1,0 +1,47 @@
+"""Precision of the linear attention's bf16 calls (GPU): what its operands may lose, and that neither the
+size of the call nor the gradients asked for beside it change a result.
+
+With `big` the sum of the absolute values of a result's terms (linattn_ref), n = T + dk + dv + 64:
+  scores, state  two bf16 terms each: the first leaves at most 2^-8 of a value, the second 2^-8 of that;
+                 2^-16 of the terms that pass through one of them, 2^-15 with room for both
+  fp32 sums      n 2^-23 big (as in the operators' other tests)
+  output         half a step of bf16, 2^-8 of the value
+A state of one term would add 2^-9 of each of its elements, at random signs 2^-9 of a result's usual
+size: beyond the bound wherever a result is small.
+"""
+import pytest
+import torch
+
+import gated_delta_rule_82_b200 as ck
+import linattn_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from gated_delta_rule_82_b200 import build
+    build.build()
+
+
+def _bound(want, big, n):
+    return ref.BF16 * want.abs() + (2.0 ** -15 + n * ref.F32) * big + 1e-30
+
+
+# (heads, head sizes: tcgen05 and warp tiles; tokens: one to many units)
+@pytest.mark.parametrize("B,T,H,Hk,dk,dv", [
+    (1, 320, 16, 16, 128, 128), (2, 700, 16, 8, 128, 128), (20, 100, 4, 4, 128, 128),
+    (1, 320, 16, 16, 64, 64), (2, 200, 32, 32, 32, 128), (1, 320, 16, 16, 128, 16),
+])
+def test_outputs_are_rounded_once(B, T, H, Hk, dk, dv):
+    d = ref.make((B, T), H, Hk, dk, dv, torch.bfloat16, states=B, seed=T + dv, grads=True, strong=0.1,
+                 device="cuda")
+    args, n = (d["q"], d["k"], d["v"], d["g"], d["h0"]), T + dk + dv + 64
+    (o, _), (big, _) = ref.forward(*args)
+    assert ref.off(ck.linattn_fwd_chunked(*args)[0], o, _bound(o, big, n)) <= 1
+    want, big = ref.backward(*args, d["do"], d["dhT"])
+    got = ck.linattn_bwd_chunked(*args, d["do"], d["dhT"])
+    for name in ("dq", "dk", "dv"):
+        assert ref.off(got[name], want[name], _bound(want[name], big[name], n)) <= 1, name
