@@ -286,7 +286,7 @@ la_run_kernel(const LaArgs a) {
     const size_t st_size = (size_t)DC * DO;
     const size_t seq_state = ((size_t)u.seq * H + h) * st_size;
     const size_t unit_state = ((size_t)unit * H + h) * st_size;
-    const bool fold = !kSummary && R.fold;
+    const bool fold = !kSummary && R.fold && R.unit_state;
     const float* init = nullptr;
     if (!kSummary) {
         if (R.unit_state && !fold) init = R.unit_state + unit_state;
@@ -298,7 +298,7 @@ la_run_kernel(const LaArgs a) {
         for (int e = 0; e < 4; ++e)
             M[n][e] = init ? init[own + (e >> 1) * 8 * rs + (8 * n + (e & 1)) * cs] : 0.f;
     if (fold) {                               // the units ahead of this one, in the run's order
-        const int ahead = rev ? min(u.count - 1 - u.index, a.sp.units - 1 - unit) : u.index;
+        const int ahead = la_units_ahead(fold, rev, unit, u.index, u.count, a.sp.units);
 #pragma unroll 1
         for (int k = 0; k < ahead; ++k) {
             const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;

@@ -12,10 +12,9 @@
 #pragma once
 
 #include "common.cuh"
+#include "linattn_units.h"
 
 namespace ckda {
-
-constexpr int kLaChunk = 64;      // tokens per chunk of the chunked form
 
 // Launch with programmatic stream serialisation: the grid may start while its predecessor in the
 // stream still runs, and calls la_wait_before() ahead of everything that the predecessor wrote (or
@@ -186,11 +185,6 @@ __device__ __forceinline__ double log2_decay(const float* g, int per_token, long
     const double x = (double)(per_token ? g[(size_t)tok * H + h] : g[h]) * 1.4426950408889634;
     return x < kLaMinLog2 ? kLaMinLog2 : x;     // (NaN stays NaN)
 }
-
-// Tokens per unit for sequences of `total` tokens (the longest `longest`) over H heads.
-int la_unit_len(long long total, long long longest, int H, int slots);
-// Units that sequences of these lengths are cut into (cu == nullptr: n rows of T tokens).
-long long la_units(const int* cu_host, int n, int T, int L);
 
 // Summaries of every unit, then the states entering every unit (needs unit_state), then the runs.
 // exact: operands that are formed in fp32 (decayed scores, states) enter the products in full

@@ -179,25 +179,6 @@ la_group_sum_kernel(const float* __restrict__ dqf, const float* __restrict__ dkf
 
 }  // namespace
 
-int la_unit_len(long long total, long long longest, int H, int slots) {
-    const long long whole = (longest + kLaChunk - 1) / kLaChunk * kLaChunk;
-    // (two chunks in turn take less time than a launch of summaries: 100 tokens, forward 19.2 us a
-    // call against 23.9 in two units; 300 tokens, 31 against 24 in five)
-    if (whole <= 2 * kLaChunk) return (int)(whole < kLaChunk ? kLaChunk : whole);
-    const int per = slots / H;          // units of all sequences that run side by side per head
-    if (per <= 1) return (int)whole;
-    long long L = ((total + per - 1) / per + kLaChunk - 1) / kLaChunk * kLaChunk;
-    if (L < kLaChunk) L = kLaChunk;
-    return (int)(L < whole ? L : whole);
-}
-
-long long la_units(const int* cu_host, int n, int T, int L) {
-    if (!cu_host) return (long long)n * ((T + (long long)L - 1) / L);
-    long long u = 0;
-    for (int s = 0; s < n; ++s) u += (cu_host[s + 1] - cu_host[s] + (long long)L - 1) / L;
-    return u;
-}
-
 // ------------------------------------------------------------------------------------ forward
 
 namespace {
@@ -212,20 +193,15 @@ FwdWs fwd_ws(void* ws, bool split, long long units, int H, int dk, int dv) {
     w.bytes = c.at;
     return w;
 }
-// more than one unit in a sequence; few enough for the runs to add the summaries up themselves
-bool is_split(const LaSplit& sp, long long longest) { return longest > sp.L; }
-bool is_folded(const LaSplit& sp, long long longest, int most) {
-    return (longest + sp.L - 1) / sp.L <= most;
-}
 }  // namespace
 
 size_t la_fwd_workspace(const LaSplit& sp, long long longest, int dk, int dv) {
-    return fwd_ws(nullptr, is_split(sp, longest), sp.units, sp.H, dk, dv).bytes;
+    return fwd_ws(nullptr, la_is_split(longest, sp.L), sp.units, sp.H, dk, dv).bytes;
 }
 
 cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv, ckda_dtype dtype,
                           void* ws, cudaStream_t s) {
-    const bool split = is_split(f.sp, longest);
+    const bool split = la_is_split(longest, f.sp.L);
     const FwdWs w = fwd_ws(ws, split, f.sp.units, f.sp.H, dk, dv);
     LaArgs a = {};
     a.sp = f.sp;
@@ -242,7 +218,7 @@ cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv,
     r.unit_state = w.states;
     r.unit_decay = w.decay;
     // (every unit reads h0 then, and the last one writes hT: not when they are the same)
-    r.fold = is_folded(f.sp, longest, kLaFoldUnits) && f.hT != f.h0;
+    r.fold = la_folds(longest, f.sp.L, kLaFoldUnits) && f.hT != f.h0;
     a.run[0] = r;
     cudaError_t e;
     if (f.sp.empty && f.hT && (!split || r.fold))
@@ -289,13 +265,13 @@ BwdWs bwd_ws(void* ws, bool split, const LaSplit& sp, long long tokens, int G, i
 
 size_t la_bwd_workspace(const LaSplit& sp, long long longest, long long tokens, int G, int dk,
                         int dv) {
-    return bwd_ws(nullptr, is_split(sp, longest), sp, tokens, G, dk, dv).bytes;
+    return bwd_ws(nullptr, la_is_split(longest, sp.L), sp, tokens, G, dk, dv).bytes;
 }
 
 cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv, ckda_dtype dtype,
                           void* ws, cudaStream_t s) {
     const LaSplit& sp = b.sp;
-    const bool split = is_split(sp, longest);
+    const bool split = la_is_split(longest, sp.L);
     const int H = sp.H, G = b.G;
     const BwdWs w = bwd_ws(ws, split, sp, b.tokens, G, dk, dv);
     cudaError_t e;
@@ -318,7 +294,7 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     // from three units on: 256 tokens x 16 heads in four 52 -> 42 us; 2 x 2048 tokens in two units 147
     // us, with a scan 151)
     const bool tc = dtype == CKDA_BF16 && dk == 128 && dv == 128;
-    const bool fold = is_folded(sp, longest, tc ? 2 : kLaFoldUnits), scan = split && !fold;
+    const bool fold = la_folds(longest, sp.L, tc ? 2 : kLaFoldUnits), scan = split && !fold;
     int parts = 1;
     if (sp.empty && b.dh0 && !scan) {
         a.run[0] = rr;

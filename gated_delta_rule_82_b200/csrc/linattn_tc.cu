@@ -413,7 +413,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         const size_t seq_state = ((size_t)u.seq * H + h) * (D * D);
         const size_t unit_state = ((size_t)unit * H + h) * (D * D);
         const size_t own = (size_t)row * rs + (size_t)col0 * cs;
-        const bool fold = !kSummary && R.fold;
+        const bool fold = !kSummary && R.fold && R.unit_state;
         const float* init = nullptr;
         if (!kSummary) {
             if (R.unit_state && !fold) init = R.unit_state + unit_state;
@@ -428,7 +428,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
         // the entering state, then (folded) the units ahead of this one, in the run's order.  Where a
         // thread's channels lie one after the other it takes four at a time (a layer's backward with
         // h0 and dhT: 176 us with single ones)
-        const int ahead = !fold ? 0 : rev ? min(u.count - 1 - u.index, a.sp.units - 1 - unit) : u.index;
+        const int ahead = la_units_ahead(fold, rev, unit, u.index, u.count, a.sp.units);
 #pragma unroll 1
         for (int k = init ? -1 : 0; k < ahead; ++k) {
             const size_t un = (size_t)(rev ? unit + ahead - k : unit - ahead + k) * H + h;
