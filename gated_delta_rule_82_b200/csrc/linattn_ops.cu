@@ -346,13 +346,12 @@ cudaError_t launch_la_bwd(const LaBwdArgs& b, long long longest, int dk, int dv,
     a.run[0] = q;
     a.run[1] = k;
     a.run[2] = v;
-    // (the decay gradient is made of differences of q.dq and k.dk: they are formed in full
-    // precision when it is asked for)
-    const bool exact = b.dg != nullptr;
+    // dq and dk in full precision: the decay gradient is made of small differences of q.dq and k.dk,
+    // and asking for it changes neither (two terms without it: 16 heads x 2 x 2048 tokens 112 us, not 134).
     // Three runs of the same kernel go in one launch, side by side.
-    const bool one = dk == dv && (dtype == CKDA_F32 || (!exact && G == 1));
+    const bool one = dk == dv && dtype == CKDA_F32;
     a.runs = one ? 3 : 2;
-    if ((e = launch_la_run(a, dv, dk, exact, dtype, s)) != cudaSuccess) return e;
+    if ((e = launch_la_run(a, dv, dk, true, dtype, s)) != cudaSuccess) return e;
     if (!one) {
         a.run[0] = v;
         a.runs = 1;

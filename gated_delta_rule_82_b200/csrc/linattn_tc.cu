@@ -1144,12 +1144,12 @@ cudaError_t launch(const LaArgs& a, cudaStream_t s) {
 cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s) {
     return launch<2, true, false, false>(a, s);
 }
-// (the runs of one launch agree in out_f32 and in having rows to multiply with; the latter are exact)
+// (the runs of one launch agree in out_f32 and in having rows to multiply with; both go with exact ones)
 cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s) {
     const bool f32 = a.run[0].out_f32, dots = a.run[0].dot != nullptr;
     if (dots) return f32 ? launch<3, false, true, true>(a, s) : launch<3, false, false, true>(a, s);
     if (exact) return f32 ? launch<3, false, true, false>(a, s) : launch<3, false, false, false>(a, s);
-    return f32 ? launch<2, false, true, false>(a, s) : launch<2, false, false, false>(a, s);
+    return launch<2, false, false, false>(a, s);
 }
 
 // Read this file's status word (`stream` has finished) and clear it.

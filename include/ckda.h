@@ -378,7 +378,8 @@ CKDA_API ckda_status ckda_linattn_fwd_chunked(
  *   dq, dk : [B, T, Hk, dk] dtype (a grouped q/k head receives the sum over its value heads)
  *   dv   : [B, T, H, dv] dtype
  *   dlog_decay : fp32, the shape of log_decay (fixed decays: the sum over all tokens), or NULL
- *                to skip it; zero where exp(g) is zero
+ *                to skip it; zero where exp(g) is zero.  dq and dk are formed with fp32-grade
+ *                products either way, and are the same bit for bit
  *   dh0  : fp32, or NULL to skip it
  *   workspace : ckda_linattn_bwd_workspace_bytes (never 0), not shared with concurrent calls.
  * Outputs must not overlap the inputs or each other; results do not depend on timing (no atomics).

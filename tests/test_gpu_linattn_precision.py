@@ -45,3 +45,16 @@ def test_outputs_are_rounded_once(B, T, H, Hk, dk, dv):
     got = ck.linattn_bwd_chunked(*args, d["do"], d["dhT"])
     for name in ("dq", "dk", "dv"):
         assert ref.off(got[name], want[name], _bound(want[name], big[name], n)) <= 1, name
+
+
+@pytest.mark.parametrize("B,T,H,Hk,dk,dv", [
+    (1, 700, 16, 16, 128, 128), (1, 700, 16, 8, 128, 128), (1, 700, 16, 16, 64, 64), (3, 100, 8, 4, 32, 16),
+])
+def test_other_gradients_do_not_change_dq_and_dk(B, T, H, Hk, dk, dv):
+    """Whether the gradients of the decays and of h0 are asked for: the same dq, dk, dv bit for bit."""
+    d = ref.make((B, T), H, Hk, dk, dv, torch.bfloat16, states=B, seed=T, grads=True, device="cuda")
+    args = (d["q"], d["k"], d["v"], d["g"], d["h0"], d["do"], d["dhT"])
+    got = ck.linattn_bwd_chunked(*args)
+    less = ck.linattn_bwd_chunked(*args, want_dlog_decay=False, want_dh0=False)
+    for name in ("dq", "dk", "dv"):
+        assert torch.equal(got[name], less[name]), name
