@@ -746,9 +746,6 @@ cudaError_t launch_la_summary(const LaArgs& a, int dc, int dout, ckda_dtype dtyp
 cudaError_t launch_la_run(const LaArgs& a, int dc, int dout, bool exact, ckda_dtype dtype,
                           cudaStream_t s) {
     if (a.sp.units == 0) return cudaSuccess;
-    // A few outputs have no averages to hide a rounded state in, and in a run of a few chunks full
-    // precision costs little (one 64-token chunk on 16 heads: 7.4 -> 9.0 us).
-    if ((long long)a.sp.units * a.sp.H * (a.sp.L / kLaChunk) <= 64) exact = true;
     if (dtype == CKDA_BF16 && dc == 128 && dout == 128) return launch_la_tc_run(a, exact, s);
     return dtype == CKDA_BF16 ? launch_type<__nv_bfloat16>(a, dc, dout, false, exact, s)
                               : launch_type<float>(a, dc, dout, false, true, s);

@@ -58,3 +58,19 @@ def test_other_gradients_do_not_change_dq_and_dk(B, T, H, Hk, dk, dv):
     less = ck.linattn_bwd_chunked(*args, want_dlog_decay=False, want_dh0=False)
     for name in ("dq", "dk", "dv"):
         assert torch.equal(got[name], less[name]), name
+
+
+@pytest.mark.parametrize("T,H,dk,dv", [(100, 2, 128, 128), (1, 16, 128, 128), (77, 4, 64, 64), (128, 2, 32, 128)])
+def test_a_sequence_alone_is_the_sequence_in_a_batch(T, H, dk, dv):
+    """Up to two chunks are one unit in any batch: the same results bit for bit, however large the call."""
+    B = 48
+    d = ref.make((B, T), H, H, dk, dv, torch.bfloat16, states=B, seed=T, grads=True, device="cuda")
+    args = [d[n] for n in ("q", "k", "v", "g", "h0")]
+    out, hT = ck.linattn_fwd_chunked(*args)
+    grads = ck.linattn_bwd_chunked(*args, d["do"], d["dhT"])
+    for b in (0, 7, B - 1):
+        one = [x[b:b + 1].contiguous() for x in (*args, d["do"], d["dhT"])]
+        o, h = ck.linattn_fwd_chunked(*one[:5])
+        assert torch.equal(o, out[b:b + 1]) and torch.equal(h, hT[b:b + 1])
+        for name, x in ck.linattn_bwd_chunked(*one).items():
+            assert torch.equal(x, grads[name][b:b + 1]), name
