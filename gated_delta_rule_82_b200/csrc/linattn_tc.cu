@@ -57,11 +57,14 @@ struct TcArgs {
     CUtensorMap out[kLaMaxRuns];          // bf16 outputs
 };
 
-// A chunk's decays, as log2 sums over its 16-token blocks that start or end at a block's edge, so
-// that no two long sums are subtracted: the decay between two tokens of different blocks is
-// r (to the end of the block) + whole blocks + l (from the start of the block).
+// A chunk's decays, as log2 sums over its 16-token blocks that start or end at a block's edge: the decay
+// between two tokens of different blocks is r (to the end of the block) + whole blocks + l (from the start
+// of the block), each a factor of at most one; that between two tokens of a block is the difference of
+// their l, which is kept in two floats: a reset adds kLaMinLog2 to the sums, and behind it differences
+// of single floats were off by 2e-4.  Summed in fp64.
 struct GateSlot {
     float l[C], r[C];        // up to and including the token; behind the token
+    float lo[C];             // what l leaves of its sum
     float out[C], upd[C];    // weights of the read-out and of the update, with their scales
     float block[4];          // whole blocks
     float total, pad[3];     // exp2 of the chunk's sum
@@ -170,9 +173,9 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, u
 }
 
 // log2 of a decay exp(g), floored as kLaMinLog2 (a NaN stays one)
-__device__ __forceinline__ float log2_decay(float g) {
-    const float x = g * 1.44269504f;
-    return x < (float)kLaMinLog2 ? (float)kLaMinLog2 : x;
+__device__ __forceinline__ double log2_decay(float g) {
+    const double x = (double)g * 1.4426950408889634;
+    return x < kLaMinLog2 ? kLaMinLog2 : x;
 }
 
 // ---- two fp32 values at a time
@@ -737,7 +740,7 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             float ra[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) ra[e] = ex2(edge[r0 + 8 * e]) * p_scale;
-            const float rl[2] = {g.l[r0], g.l[r0 + 8]};
+            const float rl[2] = {g.l[r0], g.l[r0 + 8]}, rlo[2] = {g.lo[r0], g.lo[r0 + 8]};
             const float sg = rev ? -1.f : 1.f;
             if (!wait(b, &b.sc_full, i & 1)) return false;
             if (i > 0 && !wait(b, &b.p_empty, (i - 1) & 1)) return false;
@@ -756,12 +759,13 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             for (int j = 0; j < 2; ++j) {
                 const int c = 16 * quarter + 8 * j + gc;
                 const float2 cl = *reinterpret_cast<const float2*>(g.l + c);
+                const float2 clo = *reinterpret_cast<const float2*>(g.lo + c);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int row = r0 + 8 * e;
                     float2& w = x[2 * j + e];
-                    w.x = (rev ? row <= c : row >= c) ? w.x * ex2(sg * (rl[e] - cl.x)) * p_scale : 0.f;
-                    w.y = (rev ? row <= c + 1 : row >= c + 1) ? w.y * ex2(sg * (rl[e] - cl.y)) * p_scale : 0.f;
+                    w.x = (rev ? row <= c : row >= c) ? w.x * ex2(sg * ((rl[e] - cl.x) + (rlo[e] - clo.x))) * p_scale : 0.f;
+                    w.y = (rev ? row <= c + 1 : row >= c + 1) ? w.y * ex2(sg * ((rl[e] - cl.y) + (rlo[e] - clo.y))) * p_scale : 0.f;
                 }
             }
             put(p, 16 * quarter, x);
@@ -836,46 +840,39 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             const int gs = i % kGateRing, live = live_of(i);
             t0 = chunk_at(min(i + 1, n - 1)) * C + 2 * lane;
             next = make_float2(load(t0), load(t0 + 1));
-            const float g0 = 2 * lane < live ? log2_decay(cur.x) : 0.f;
-            const float g1 = 2 * lane + 1 < live ? log2_decay(cur.y) : 0.f;
-            float pre = g0 + g1, suf = pre;                       // over the 8 lanes of a block
+            const double g0 = 2 * lane < live ? log2_decay(cur.x) : 0.0;
+            const double g1 = 2 * lane + 1 < live ? log2_decay(cur.y) : 0.0;
+            double upto = g0 + g1;                                // since the start of the chunk
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-                const float x = __shfl_up_sync(0xffffffffu, pre, o, 8), y = __shfl_down_sync(0xffffffffu, suf, o, 8);
-                if ((lane & 7) >= o) pre += x;
-                if ((lane & 7) + o < 8) suf += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
             }
-            float before = __shfl_up_sync(0xffffffffu, pre, 1, 8), after = __shfl_down_sync(0xffffffffu, suf, 1, 8);
-            if ((lane & 7) == 0) before = 0.f;
-            if ((lane & 7) == 7) after = 0.f;
-            float blk[4], ahead = 0.f, behind = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                blk[k] = __shfl_sync(0xffffffffu, pre, 8 * k + 7);
-                ahead += k < (lane >> 3) ? blk[k] : 0.f;
-                behind += k > (lane >> 3) ? blk[k] : 0.f;
-            }
-            const float all = (blk[0] + blk[1]) + (blk[2] + blk[3]);
-            if constexpr (kSummary) decay += (double)all;
+            const double all = __shfl_sync(0xffffffffu, upto, 31);
+            const double end = __shfl_sync(0xffffffffu, upto, lane | 7);        // of this lane's block
+            double start = __shfl_sync(0xffffffffu, upto, max((lane & ~7) - 1, 0));
+            if (lane < 8) start = 0.0;
+            if constexpr (kSummary) decay += all;
             if (i >= kGateRing && !wait(b, &b.gempty[gs], (i / kGateRing - 1) & 1)) break;
             GateSlot& g = gates[gs];
-            const float2 l = make_float2(before + g0, pre), r = make_float2(g1 + after, after);
-            const float2 down = make_float2(ex2(ahead + l.x), ex2(ahead + l.y));     // since the start
-            const float2 up = make_float2(ex2(r.x + behind), ex2(r.y + behind));     // to the end
+            const double G0 = upto - g1;
+            const float2 down = make_float2(ex2((float)G0), ex2((float)upto));                  // since the start
+            const float2 up = make_float2(ex2((float)(all - G0)), ex2((float)(all - upto)));    // to the end
             const float2 w = rev ? down : up;
             const int t = 2 * lane;
             *reinterpret_cast<float2*>(g.upd + t) =
                 make_float2(t < live ? w.x * u_scale : 0.f, t + 1 < live ? w.y * u_scale : 0.f);
             if constexpr (!kSummary) {
+                const double l0 = G0 - start, l1 = upto - start;
+                const float2 l = make_float2((float)l0, (float)l1);
                 *reinterpret_cast<float2*>(g.l + t) = l;
-                *reinterpret_cast<float2*>(g.r + t) = r;
+                *reinterpret_cast<float2*>(g.lo + t) = make_float2((float)(l0 - l.x), (float)(l1 - l.y));
+                *reinterpret_cast<float2*>(g.r + t) = make_float2((float)(end - G0), (float)(end - upto));
+                if ((lane & 7) == 7) g.block[lane >> 3] = l.y;
                 const float2 o = rev ? up : down;
                 *reinterpret_cast<float2*>(g.out + t) = make_float2(o.x * o_scale, o.y * o_scale);
             }
-            if (lane == 0) {
-                g.total = ex2(all);
-                *reinterpret_cast<float4*>(g.block) = make_float4(blk[0], blk[1], blk[2], blk[3]);
-            }
+            if (lane == 0) g.total = ex2((float)all);
             arrive_warp(&b.gfull[gs]);
             // (three chunks behind, so that the element warps never wait for this)
             if constexpr (dots)

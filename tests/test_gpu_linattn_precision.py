@@ -74,3 +74,29 @@ def test_a_sequence_alone_is_the_sequence_in_a_batch(T, H, dk, dv):
         assert torch.equal(o, out[b:b + 1]) and torch.equal(h, hT[b:b + 1])
         for name, x in ck.linattn_bwd_chunked(*one).items():
             assert torch.equal(x, grads[name][b:b + 1]), name
+
+
+def _neighbours(B, T, H, d):
+    """q_t = do_t = e_{t-1}, k_t = v_t = e_t: the only products are those of a token with the one before
+    it, and dlog_decay_t is the decay between them."""
+    eye = torch.eye(d, dtype=torch.bfloat16, device="cuda")
+    rows = lambda first: eye[(torch.arange(T) + first) % d].view(1, T, 1, d).expand(B, T, H, d).contiguous()
+    return rows(d - 1), rows(0), rows(0), rows(d - 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("forget", [-float("inf"), -80.0])
+@pytest.mark.parametrize("T,at", [(16, range(12)), (16, [3, 4, 5, 6, 9]), (60, [0, 17, 18, 19, 20, 35, 36, 37, 38])])
+def test_decays_behind_resets(T, at, forget, d):
+    """Decays behind resets (or behind tokens that forget all but e^-80) of the same 16 tokens.  Every
+    product has one term that is not zero, so a row of q.dq or k.dk has the roundings of its decay alone: of
+    the exponent (2^-24 of at most 2), of 2^x (2^-22) and of three-term operands (2^-24), together below
+    4 2^-23; 8 2^-23 of the sum of the later rows bounds their differences.  (Differences of single floats
+    of -1000 were off by 1e-4.)"""
+    B, H = 24, 2
+    q, k, v, do = _neighbours(B, T, H, d)
+    g = -torch.rand(B, T, H, generator=torch.Generator().manual_seed(T)).cuda()
+    g[:, list(at)] = forget
+    want, big = ref.backward(q, k, v, g, None, do, None, scale=1.0)
+    got = ck.linattn_bwd_chunked(q, k, v, g, None, do, scale=1.0)
+    assert ref.off(got["dlog_decay"], want["dlog_decay"], 8 * ref.F32 * big["dlog_decay"] + 1e-30) <= 1
