@@ -806,21 +806,22 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             if (!wait(b, &b.dot_full[slot], (i / kGateRing) & 1)) return false;
             const int c = chunk_at(i), live = live_of(i);
             const long long tok = u.tok + (long long)c * C;
-            float sum = 0.f;
+            double sum = 0.0;      // (a gradient is a small difference of these sums)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 32 * e + lane;
                 const float s = (d[t] + d[C + t]) + (d[2 * C + t] + d[3 * C + t]);
                 if (t < live) {
                     R.dot_out[(size_t)(tok + t) * H + h] = s;
-                    sum += s;
+                    sum += (double)s;
                 }
             }
             arrive_warp(&b.dot_empty[slot]);
-            sum = warp_sum(sum);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0)
                 R.dot_sum[(size_t)la_chunk_id(u.tok - (long long)u.index * a.sp.L, u.seq,
-                                              u.index * (a.sp.L / C) + c) * H + h] = (double)sum;
+                                              u.index * (a.sp.L / C) + c) * H + h] = sum;
             return true;
         };
         const float u_scale = R.u_scale, o_scale = R.o_scale;

@@ -100,3 +100,25 @@ def test_decays_behind_resets(T, at, forget, d):
     want, big = ref.backward(q, k, v, g, None, do, None, scale=1.0)
     got = ck.linattn_bwd_chunked(q, k, v, g, None, do, scale=1.0)
     assert ref.off(got["dlog_decay"], want["dlog_decay"], 8 * ref.F32 * big["dlog_decay"] + 1e-30) <= 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_sums_of_the_decay_gradient(d, dtype):
+    """Whole numbers, no decay: rows of q.dq and k.dk stay below 2^24 and are exact, their sums over a chunk
+    pass 2^27, and the gradients, differences of those, come out exactly (0 before the first key)."""
+    T, H = 128, 3
+    gen = torch.Generator().manual_seed(d)
+    q, k, v, do = (torch.randint(0, 4, (1, T, H, d), generator=gen).to(dtype) for _ in range(4))
+    for x in (q, k, v, do):
+        x[:, :63] = 0
+    for x in (k, v):
+        x[:, 63] = 0
+        x[:, 63, :, 0] = 1
+    q, k, v, do = (x.cuda() for x in (q, k, v, do))
+    g = torch.zeros(1, T, H, device="cuda")
+    want, _ = ref.backward(q, k, v, g, None, do, None, scale=1.0)
+    rows = (ref.expand(q, k, g, H)[0].double().cpu() * want["dq"]).sum(-1)
+    assert float(rows.max()) < 2 ** 24 and (d < 128 or float(rows.sum(1).max()) > 2 ** 27)
+    got = ck.linattn_bwd_chunked(q, k, v, g, None, do, scale=1.0)
+    assert torch.equal(got["dlog_decay"].cpu(), want["dlog_decay"].float())
