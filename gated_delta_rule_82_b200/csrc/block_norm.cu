@@ -507,11 +507,13 @@ int rows_per_cta(int D) {
     return t < 128 ? 128 / t : 1;
 }
 
-// Dynamic shared memory above the default needs the attribute, per kernel and device.
-template <typename K>
-cudaError_t room(K kern, size_t bytes) {
-    return bytes > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    (int)bytes)
+// Dynamic shared memory above the default needs the attribute, per kernel and device.  Always for the
+// most that rows of TPR threads can ask for (three weight vectors): set to a call's own need, it fell
+// below that of a call that another host thread was about to launch.
+template <int TPR, typename K>
+cudaError_t room(K kern) {
+    constexpr int kMost = 3 * TPR * E * (int)sizeof(float);
+    return kMost > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)
                              : cudaSuccess;
 }
 
@@ -523,7 +525,7 @@ cudaError_t fwd_t(const BlockNormArgs& p, cudaStream_t s) {
     auto kern = p.act == kActSilu      ? block_norm_kernel<T, TPR, kVec, kActSilu>
                 : p.act == kActSigmoid ? block_norm_kernel<T, TPR, kVec, kActSigmoid>
                                        : block_norm_kernel<T, TPR, kVec, kActNone>;
-    const cudaError_t e = room(kern, smem);
+    const cudaError_t e = room<TPR>(kern);
     if (e != cudaSuccess) return e;
     kern<<<(int)(ctas < most ? ctas : most), THREADS, smem, s>>>(p);
     return cudaGetLastError();
@@ -537,7 +539,7 @@ cudaError_t bwd_t(const BlockNormArgs& p, const BlockNormGrads& g, int grid, cud
     auto kern = p.act == kActSilu      ? block_norm_bwd_kernel<T, TPR, kVec, kActSilu>
                 : p.act == kActSigmoid ? block_norm_bwd_kernel<T, TPR, kVec, kActSigmoid>
                                        : block_norm_bwd_kernel<T, TPR, kVec, kActNone>;
-    const cudaError_t e = room(kern, smem);
+    const cudaError_t e = room<TPR>(kern);
     if (e != cudaSuccess) return e;
     kern<<<grid, THREADS, smem, s>>>(p, g);
     return cudaGetLastError();
