@@ -301,15 +301,23 @@ def fwd_segmented(q, k, v, alpha, beta, h0=None, *, segments=0, l2norm=True, rop
     return out, hT
 
 
+def _offsets(host):
+    """Host offsets as int32 (the library reads them where they lie)."""
+    if not isinstance(host, torch.Tensor):
+        raise TypeError("cu_seqlens_cpu must be a torch.Tensor")
+    if host.device.type != "cpu":
+        raise ValueError("cu_seqlens_cpu is not on the CPU")
+    if host.numel() < 2:
+        raise ValueError("cu_seqlens_cpu: expected [n + 1] token offsets, n >= 1")
+    return host.to(torch.int32).contiguous()
+
+
 def _host_offsets(cu_seqlens, cu_seqlens_cpu):
     """int32 offsets on the device (as given) and a host copy (given, or read back: a sync)."""
     _check(cu_seqlens, "cu_seqlens", dtype=torch.int32)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens: expected [n + 1] token offsets, n >= 1")
-    host = cu_seqlens.cpu() if cu_seqlens_cpu is None else cu_seqlens_cpu
-    if host.device.type != "cpu":
-        raise ValueError("cu_seqlens_cpu is not on the CPU")
-    host = host.to(torch.int32).contiguous()
+    host = _offsets(cu_seqlens.cpu() if cu_seqlens_cpu is None else cu_seqlens_cpu)
     if tuple(host.shape) != tuple(cu_seqlens.shape):
         raise ValueError("cu_seqlens_cpu must have the shape of cu_seqlens")
     return host
@@ -317,7 +325,7 @@ def _host_offsets(cu_seqlens, cu_seqlens_cpu):
 
 def varlen_workspace_bytes(cu_seqlens_cpu, H, dk, dv, chunk, dtype, path="auto") -> int:
     """Device workspace bytes of fwd_varlen for these host offsets (0 when none is needed)."""
-    host = cu_seqlens_cpu.to(torch.int32).contiguous()
+    host = _offsets(cu_seqlens_cpu)
     code = _BF16 if dtype == torch.bfloat16 else _F32
     n = _load().ckda_fwd_varlen_workspace_bytes(ctypes.c_void_p(host.data_ptr()), host.numel() - 1,
                                                 H, dk, dv, chunk, code, PATHS[path])
@@ -540,7 +548,7 @@ def _linattn_shapes(q, k, v, log_decay, cu_seqlens, cu_seqlens_cpu):
 def linattn_fwd_workspace_bytes(B, T, H, dk, dv, cu_seqlens_cpu=None) -> int:
     """Device workspace bytes of linattn_fwd_chunked: B rows of T tokens, or (B and T ignored)
     packed sequences with these host offsets.  0 when none is needed."""
-    host = None if cu_seqlens_cpu is None else cu_seqlens_cpu.to(torch.int32).contiguous()
+    host = None if cu_seqlens_cpu is None else _offsets(cu_seqlens_cpu)
     n = _load().ckda_linattn_fwd_workspace_bytes(B, T, _ptr(host),
                                                  0 if host is None else host.numel() - 1, H, dk, dv)
     if n == ctypes.c_size_t(-1).value:
@@ -592,7 +600,7 @@ def linattn_fwd_chunked(q, k, v, log_decay, h0=None, *, cu_seqlens=None, cu_seql
 
 def linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv, cu_seqlens_cpu=None) -> int:
     """Device workspace bytes of linattn_bwd_chunked (arguments as the forward's query)."""
-    host = None if cu_seqlens_cpu is None else cu_seqlens_cpu.to(torch.int32).contiguous()
+    host = None if cu_seqlens_cpu is None else _offsets(cu_seqlens_cpu)
     n = _load().ckda_linattn_bwd_workspace_bytes(B, T, _ptr(host),
                                                  0 if host is None else host.numel() - 1, H, Hk, dk,
                                                  dv)

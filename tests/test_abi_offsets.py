@@ -1,0 +1,34 @@
+"""Host offsets of packed sequences, which the library reads on the host: those that do not lie there, or
+are no offsets, are refused by the workspace queries too.  CPU only."""
+import pytest
+import torch
+
+import gated_delta_rule_82_b200 as ck
+
+QUERIES = [lambda cu: ck.linattn_fwd_workspace_bytes(1, 500, 2, 16, 32, cu),
+           lambda cu: ck.linattn_bwd_workspace_bytes(1, 500, 2, 2, 16, 32, cu),
+           lambda cu: ck.varlen_workspace_bytes(cu, 2, 16, 32, 64, torch.float32)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_delta_rule_82_b200 import build
+    build.build()
+
+
+@pytest.mark.parametrize("query", QUERIES)
+@pytest.mark.parametrize("cu,error", [
+    (torch.empty(3, dtype=torch.int32, device="meta"), ValueError),      # not host memory
+    (torch.empty(0, dtype=torch.int32), ValueError), (torch.tensor([0], dtype=torch.int32), ValueError),
+    ([0, 3, 9], TypeError),
+])
+def test_offsets_that_are_not_on_the_host(query, cu, error):
+    with pytest.raises(error):
+        query(cu)
+
+
+@pytest.mark.parametrize("query", QUERIES)
+def test_offsets_of_any_integer_type(query):
+    want = query(torch.tensor([0, 300, 301, 900], dtype=torch.int32))
+    wide = torch.tensor([0, 7, 300, 7, 301, 7, 900], dtype=torch.int64)[::2]     # (strided, too)
+    assert query(wide) == want
