@@ -148,6 +148,19 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _room(workspace, device):
+    """(address, bytes) of a workspace that a caller gave, or (None, 0)."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if not workspace.is_contiguous():     # (its bytes are counted by its elements)
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -227,13 +240,13 @@ def fwd_chunked(q, k, v, alpha, beta, h0=None, *, chunk=64, l2norm=True, rope_th
             need = int(_load().ckda_fwd_simt_workspace_bytes(B, T, H, dk, dv))
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    room = _room(workspace, q.device)
     st = _load().ckda_fwd_chunked(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(out), _ptr(hT),
         B, T, H, dk, dv, int(chunk), _flags(l2norm, rope_theta, rope_convention, scale,
                                            PATHS[path], stages, gate_logits,
                                            Hk if Hk != H else 0, rope_dims),
-        code, int(pos_offset), _ptr(workspace), wbytes, _stream(q.device))
+        code, int(pos_offset), *room, _stream(q.device))
     _raise("ckda_fwd_chunked", st)
     return out, hT
 
@@ -290,12 +303,12 @@ def fwd_segmented(q, k, v, alpha, beta, h0=None, *, segments=0, l2norm=True, rop
     if workspace is None:
         workspace = torch.empty(segmented_workspace_bytes(B, T, H, dk, dv, segments),
                                 dtype=torch.uint8, device=q.device)
-    wbytes = workspace.numel() * workspace.element_size()
+    room = _room(workspace, q.device)
     st = _load().ckda_fwd_segmented(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(out), _ptr(hT),
         B, T, H, dk, dv, _flags(l2norm, rope_theta, rope_convention, scale, PATHS["tc"], 0,
                                 gate_logits, Hk if Hk != H else 0, rope_dims),
-        _dtype_code(q), int(pos_offset), int(segments), _ptr(workspace), wbytes,
+        _dtype_code(q), int(pos_offset), int(segments), *room,
         _stream(q.device))
     _raise("ckda_fwd_segmented", st)
     return out, hT
@@ -379,13 +392,13 @@ def fwd_varlen(q, k, v, alpha, beta, cu_seqlens, h0=None, *, cu_seqlens_cpu=None
         need = varlen_workspace_bytes(host, H, dk, dv, chunk, q.dtype, path)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    room = _room(workspace, q.device)
     st = _load().ckda_fwd_varlen(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(out), _ptr(hT),
         _ptr(cu_seqlens), ctypes.c_void_p(host.data_ptr()), n, H, dk, dv, int(chunk),
         _flags(l2norm, rope_theta, rope_convention, scale, PATHS[path], stages, gate_logits,
                Hk if Hk != H else 0, rope_dims),
-        _dtype_code(q), int(pos_offset), _ptr(workspace), wbytes, _stream(q.device))
+        _dtype_code(q), int(pos_offset), *room, _stream(q.device))
     _raise("ckda_fwd_varlen", st)
     return out, hT
 
@@ -459,14 +472,14 @@ def bwd_chunked(q, k, v, alpha, beta, h0, dout, dhT=None, *, l2norm=True, rope_t
     if workspace is None:
         workspace = torch.empty(bwd_workspace_bytes(B, T, H, dk, dv), dtype=torch.uint8,
                                 device=q.device)
-    wbytes = workspace.numel() * workspace.element_size()
+    room = _room(workspace, q.device)
     st = _load().ckda_bwd_chunked(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(h0), _ptr(dout), _ptr(dhT),
         _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dalpha"]), _ptr(g["dbeta"]),
         _ptr(g["dh0"]), B, T, H, dk, dv,
         _flags(l2norm, rope_theta, rope_convention, scale, 0, 0, gate_logits,
                Hk if Hk != H else 0, rope_dims),
-        _dtype_code(q), int(pos_offset), _ptr(workspace), wbytes, _stream(q.device))
+        _dtype_code(q), int(pos_offset), *room, _stream(q.device))
     _raise("ckda_bwd_chunked", st)
     return g
 
@@ -586,14 +599,11 @@ def linattn_fwd_chunked(q, k, v, log_decay, h0=None, *, cu_seqlens=None, cu_seql
                 else linattn_fwd_workspace_bytes(B, T, H, dk, dv, host))
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, q on {dev}")
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    room = _room(workspace, dev)
     st = _call(_load().ckda_linattn_fwd_chunked, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                log_decay.data_ptr(), int(per_token), _p(h0), out.data_ptr(), _p(hT), B, T,
                _p(cu_seqlens), _p(host), 0 if host is None else n, H, dk, dv,
-               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q), _p(workspace),
-               wbytes)
+               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q), *room)
     _raise("ckda_linattn_fwd_chunked", st)
     return out, hT
 
@@ -633,14 +643,12 @@ def linattn_bwd_chunked(q, k, v, log_decay, h0, dout, dhT=None, *, cu_seqlens=No
         need = (_linattn_rows_bytes(True, B, T, H, Hk, dk, dv) if host is None
                 else linattn_bwd_workspace_bytes(B, T, H, Hk, dk, dv, host))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, q on {dev}")
+    room = _room(workspace, dev)
     st = _call(_load().ckda_linattn_bwd_chunked, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                log_decay.data_ptr(), int(per_token), _p(h0), dout.data_ptr(), _p(dhT),
                g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), _p(g["dlog_decay"]),
                _p(g["dh0"]), B, T, _p(cu_seqlens), _p(host), 0 if host is None else n, H, dk, dv,
-               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q),
-               workspace.data_ptr(), workspace.numel() * workspace.element_size())
+               _linattn_flags(float(scale), Hk if Hk != H else 0), _dtype_code(q), *room)
     _raise("ckda_linattn_bwd_chunked", st)
     return g
 
@@ -774,8 +782,6 @@ def block_norm_bwd(y, dh, dn=None, *, gate=None, gate_act="none", residual=None,
         _need(dh, "dh", y.dtype, y.shape, y.device)
     if dn is not None:
         _need(dn, "dn", y.dtype, y.shape, y.device)
-    if workspace is not None and workspace.device != y.device:
-        raise ValueError(f"workspace is on {workspace.device}, y on {y.device}")
     like = lambda t: None if t is None else torch.empty_like(t)
     g = {"dy": torch.empty_like(y), "dgate": like(gate), "dresidual": like(residual),
          "dpost_weight": like(post_weight), "dres_vector": like(res_vector), "dpre_weight": None}
@@ -786,12 +792,12 @@ def block_norm_bwd(y, dh, dn=None, *, gate=None, gate_act="none", residual=None,
     if workspace is None and sums:
         workspace = torch.empty(block_norm_bwd_workspace_bytes(rows, D, post_group),
                                 dtype=torch.uint8, device=y.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    room = _room(workspace, y.device)
     st = _call(_load().ckda_block_norm_bwd, y.device, y.data_ptr(), _p(gate), _p(residual),
                _p(post_weight), _p(res_vector), _p(pre_weight), _p(dh), _p(dn), g["dy"].data_ptr(),
                _p(g["dgate"]), _p(g["dresidual"]), _p(g["dpost_weight"]), _p(g["dres_vector"]),
                _p(g["dpre_weight"]) if dn is not None else None, rows, D, flags, _dtype_code(y),
-               _p(workspace), wbytes)
+               *room)
     _raise("ckda_block_norm_bwd", st)
     return g
 

@@ -32,3 +32,18 @@ def test_offsets_of_any_integer_type(query):
     want = query(torch.tensor([0, 300, 301, 900], dtype=torch.int32))
     wide = torch.tensor([0, 7, 300, 7, 301, 7, 900], dtype=torch.int64)[::2]     # (strided, too)
     assert query(wide) == want
+
+
+@pytest.mark.parametrize("workspace,error", [
+    (torch.empty(1, dtype=torch.uint8).expand(1 << 20), ValueError),      # a million elements of one byte
+    (torch.empty(64, dtype=torch.uint8)[::2], ValueError),
+    (torch.empty(64, dtype=torch.uint8, device="meta"), ValueError), (bytearray(64), TypeError),
+])
+def test_workspaces_that_are_not_what_they_count(workspace, error):
+    with pytest.raises(error):
+        ck._room(workspace, torch.device("cpu"))
+
+
+def test_workspace_bytes():
+    w = torch.empty(10, dtype=torch.float64)
+    assert ck._room(w, torch.device("cpu")) == (w.data_ptr(), 80) and ck._room(None, torch.device("cpu")) == (None, 0)

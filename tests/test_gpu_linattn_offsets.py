@@ -59,3 +59,34 @@ def test_offsets_that_disagree_stay_inside(host, device, H, Hk, dk, dv, dtype):
         if x.dtype == torch.bfloat16:
             bound = bound + ref.BF16 * (want.abs() + big)
         assert ref.off(x, want, bound) <= 1
+
+
+def test_workspaces_given_are_checked():
+    """One that repeats a byte, lies on the host, or is one byte short is refused by every call; one of
+    exactly the bytes asked for serves."""
+    T, H, d = 900, 4, 128
+    x = ref.make((1, T), H, H, d, d, torch.bfloat16, seed=1, grads=True, device="cuda")
+    args, y = (x["q"], x["k"], x["v"], x["g"]), x["v"].view(T, H * d)
+    w = torch.ones(H * d, device="cuda")
+    f32 = [t.float() for t in args]
+    calls = [
+        (ck.linattn_fwd_workspace_bytes(1, T, H, d, d),
+         lambda ws: [ck.linattn_fwd_chunked(*a, workspace=ws)[0] for a in (args, f32)]),
+        (ck.linattn_bwd_workspace_bytes(1, T, H, H, d, d),
+         lambda ws: [ck.linattn_bwd_chunked(*a, None, x["do"].to(a[0].dtype), workspace=ws)["dq"]
+                     for a in (args, f32)]),
+        (ck.block_norm_bwd_workspace_bytes(T, H * d),
+         lambda ws: [ck.block_norm_bwd(y, y, y, pre_norm=True, pre_weight=w, workspace=ws)["dy"]]),
+    ]
+    for need, call in calls:
+        one = torch.empty(1, dtype=torch.uint8, device="cuda")
+        for bad in (one.expand(need), torch.empty(need, dtype=torch.uint8)):
+            with pytest.raises(ValueError):
+                call(bad)
+        buf = torch.empty(need, dtype=torch.uint8, device="cuda")
+        # (the query is the need of the type that takes more: for that one a byte less is too little)
+        with pytest.raises(ck.CkdaError) as e:
+            call(buf[:need - 1])
+        assert e.value.status == 5
+        for got, want in zip(call(buf), call(None)):
+            assert torch.equal(got, want)
