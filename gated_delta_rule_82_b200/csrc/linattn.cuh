@@ -157,15 +157,15 @@ __device__ inline void seq_units(const LaSplit& sp, int seq, int* first, int* co
             m = (b - a + sp.L - 1) / sp.L;
         }
         if (s == seq) own = m;
-        before += s < seq ? m : 0;
+        if (s < seq) before = la_add_units(before, m, sp.units);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
+        before = la_add_units(before, __shfl_xor_sync(0xffffffffu, before, o), sp.units);
         own += __shfl_xor_sync(0xffffffffu, own, o);
     }
-    *first = min(before, sp.units);
-    *count = min(own, sp.units - *first);
+    *first = before;
+    *count = min(own, sp.units - before);
 }
 
 // Number of a sequence's chunk among all chunks: distinct for every (sequence, chunk), because

@@ -45,6 +45,12 @@ inline bool la_folds(long long longest, int L, int most) {
     return la_is_split(longest, L) && (longest + L - 1) / L <= most;
 }
 
+// Units counted so far and a sequence's `more`, at most `units` in all: offsets in device memory that
+// differ from the host's may give any number of sequences the whole token axis.
+CKDA_HD_UNITS int la_add_units(int so_far, int more, int units) {
+    return more < units - so_far ? so_far + more : units;
+}
+
 // Units of its sequence that a run has behind it when it enters unit `unit`, number `index` of the
 // sequence's `count`.  `index` and `count` follow the offsets in device memory, which may differ from
 // the host's that summaries and workspace were planned for: nothing is summed up where there are no

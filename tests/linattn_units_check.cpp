@@ -49,6 +49,20 @@ int main() {
             before += count;
         }
     }
+    // units of the sequences ahead of one, a lane's and then the warp's, where each is the whole axis
+    for (int n : {1, 1000, 1 << 22})
+        for (int units : {1, 977, 1 << 27}) {
+            const int each = (1 << 25) / (n > 1000 ? 4 : 1);
+            int lane[32] = {};
+            for (int s = 0; s < n; ++s) lane[s % 32] = la_add_units(lane[s % 32], each, units);
+            for (int o = 16; o > 0; o >>= 1) {
+                int sum[32];
+                for (int i = 0; i < 32; ++i) sum[i] = la_add_units(lane[i], lane[i ^ o], units);
+                std::copy(sum, sum + 32, lane);
+            }
+            for (int x : lane) bad += x != std::min<long long>((long long)n * each, units);
+            ++cases;
+        }
     std::printf("cases %ld folds %ld bad %ld\n", cases, folds, bad);
     return bad != 0 || folds < 100;
 }
