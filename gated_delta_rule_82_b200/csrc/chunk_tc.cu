@@ -2206,21 +2206,20 @@ cudaError_t launch_chunk_tc_seg(const void* q, const void* k, const void* v, con
                               outb, hT, T_len, H, NT, BH, scale, sa);
 }
 
-// Read the status word on the current device (after `stream` has finished) and clear it.
+// Read the status word on the current device (after `stream` has finished) and clear it.  The linear
+// attention's is moved into it first (23 us a call; with a second copy to the host 28.5).
 cudaError_t device_status_take(cudaStream_t stream, int* code) {
     int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_tc_error, sizeof(int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
+    void* word = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&word, g_tc_error);
+    if (e == cudaSuccess) e = la_status_move(static_cast<int*>(word), stream);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&v, word, sizeof(int), cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e == cudaSuccess && v != 0) {
-        static const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_tc_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
-                                    stream);
+        e = cudaMemsetAsync(word, 0, sizeof(int), stream);
         if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     }
-    int la = 0;      // (the linear attention's word)
-    if (e == cudaSuccess) e = la_status_take(stream, &la);
-    *code = v ? v : la;
+    *code = v;
     return e;
 }
 

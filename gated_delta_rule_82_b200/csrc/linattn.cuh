@@ -191,11 +191,12 @@ __device__ __forceinline__ double log2_decay(const float* g, int per_token, long
 // precision; otherwise rounded once to bf16 (bf16 inputs only).
 cudaError_t launch_la_summary(const LaArgs& a, int dc, int dout, ckda_dtype dtype, cudaStream_t s);
 // The same summaries and runs on the tcgen05 tensor cores: bf16, 128 x 128 heads (linattn_tc.cu).
-// A wait of theirs that runs out is kept as kLaStatusWait until la_status_take.
+// A wait of theirs that runs out is kept as kLaStatusWait on the current device, until la_status_move hands
+// it to a status word that holds no other.
 constexpr int kLaStatusWait = 4;
 cudaError_t launch_la_tc_summary(const LaArgs& a, cudaStream_t s);
 cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s);
-cudaError_t la_status_take(cudaStream_t stream, int* code);
+cudaError_t la_status_move(int* word, cudaStream_t stream);
 
 // Up to this many units a sequence, a run forms its entering state itself (from a few 64 KB summaries
 // in L2) instead of a launch of its own for the scan: 4 units of 512 tokens 41.1 -> 38.8 us, 8 units

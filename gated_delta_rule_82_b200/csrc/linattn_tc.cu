@@ -1076,6 +1076,11 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
     if (warp == S::EXTRA + 1) tc::tmem_dealloc(tmem, 512);
 }
 
+__global__ void la_status_move_kernel(int* word) {
+    const int v = atomicExch(&g_la_status, 0);
+    if (v != 0) atomicCAS(word, 0, v);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void* p = nullptr;
@@ -1150,20 +1155,9 @@ cudaError_t launch_la_tc_run(const LaArgs& a, bool exact, cudaStream_t s) {
     return launch<2, false, false, false>(a, s);
 }
 
-// Read this file's status word (`stream` has finished) and clear it.
-cudaError_t la_status_take(cudaStream_t stream, int* code) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_la_status, sizeof(int), 0,
-                                              cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e == cudaSuccess && v != 0) {
-        static const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_la_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
-                                    stream);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    }
-    *code = v;
-    return e;
+cudaError_t la_status_move(int* word, cudaStream_t stream) {
+    la_status_move_kernel<<<1, 1, 0, stream>>>(word);
+    return cudaGetLastError();
 }
 
 }  // namespace ckda
