@@ -803,12 +803,14 @@ def block_norm_bwd(y, dh, dn=None, *, gate=None, gate_act="none", residual=None,
 
 
 def last_device_status(device=None) -> int:
-    """Wait for the current stream, then read and clear the library's device status word:
+    """Wait for the current stream of `device` (or of the current one), then read and clear the
+    library's status word there:
     0 = no failure recorded; 1 / 2 = a bounded wait of the tensor-core forward ran out (factor
     work / state pass); 3 = packed-sequence offsets on the device disagreed with the host copy; 4 = a
     bounded wait of the linear attention's tensor-core kernels ran out."""
     code = ctypes.c_int(0)
-    st = _load().ckda_last_device_status(_stream(device), ctypes.byref(code))
+    with torch.cuda.device(device):     # (each device has a word of its own)
+        st = _load().ckda_last_device_status(_stream(device), ctypes.byref(code))
     if st not in (0, 8):   # CKDA_OK, CKDA_ERR_DEVICE_STATUS
         raise CkdaError("ckda_last_device_status", st)
     return int(code.value)

@@ -47,3 +47,31 @@ def test_workspaces_that_are_not_what_they_count(workspace, error):
 def test_workspace_bytes():
     w = torch.empty(10, dtype=torch.float64)
     assert ck._room(w, torch.device("cpu")) == (w.data_ptr(), 80) and ck._room(None, torch.device("cpu")) == (None, 0)
+
+
+def test_device_status_is_read_on_the_device_asked_for(monkeypatch):
+    """(with a fake library and fake devices: the word belongs to the device that is current)"""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before = current[0]
+            current[0] = current[0] if self.index is None else self.index
+
+        def __exit__(self, *error):
+            current[0] = self.before
+
+    class Library:
+        @staticmethod
+        def ckda_last_device_status(stream, code):
+            seen.append((current[0], stream))
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ck, "_load", lambda: Library)
+    monkeypatch.setattr(ck, "_stream", lambda device: f"stream of {current[0] if device is None else device}")
+    assert ck.last_device_status(2) == 0 and ck.last_device_status() == 0
+    assert seen == [(2, "stream of 2"), (0, "stream of 0")] and current == [0]
