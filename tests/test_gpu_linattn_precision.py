@@ -122,3 +122,28 @@ def test_sums_of_the_decay_gradient(d, dtype):
     assert float(rows.max()) < 2 ** 24 and (d < 128 or float(rows.sum(1).max()) > 2 ** 27)
     got = ck.linattn_bwd_chunked(q, k, v, g, None, do, scale=1.0)
     assert torch.equal(got["dlog_decay"].cpu(), want["dlog_decay"].float())
+
+
+def test_sums_of_the_decay_gradient_past_32_bits():
+    """The same behind 2^31 elements: tokens of zeros, then some of whole numbers; the gradients of the last
+    tokens are exact, and 0 on all before them."""
+    torch.cuda.empty_cache()
+    T, H, d, tail = 1_060_001, 16, 128, 150
+    gen = torch.Generator().manual_seed(1)
+    part = [torch.randint(0, 4, (1, tail, H, d), generator=gen).bfloat16() for _ in range(4)]
+    full = [torch.zeros(1, T, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    for x, p in zip(full, part):
+        x[:, -tail:] = p.cuda()
+    q, k, v, do = full
+    want, _ = ref.backward(*part[:3], torch.zeros(1, tail, H), None, part[3], None, scale=1.0)
+    got = ck.linattn_bwd_chunked(q, k, v, torch.zeros(1, T, H, device="cuda"), None, do, scale=1.0)
+    rows = [(part[0].double() * want["dq"]).sum(-1), (part[1].double() * want["dk"]).sum(-1)]
+    assert float(max(x.max() for x in rows)) < 2 ** 24
+    dg = got["dlog_decay"]
+    assert torch.equal(dg[:, -tail:].cpu(), want["dlog_decay"].float())
+    assert bool((dg[:, :-tail] == 0).all())
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(got[n][:, -tail:].cpu(), want[n].to(torch.bfloat16)), n
+        assert not bool(got[n][:, :-tail].any()), n
+    del full, q, k, v, do, got
+    torch.cuda.empty_cache()
