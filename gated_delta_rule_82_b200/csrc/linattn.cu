@@ -88,7 +88,7 @@ struct RunShape {
     static constexpr int STAGE = NI * (XY * (kSummary ? 1 : 2) + Z);
     static constexpr int PP = kSummary ? 0 : NP * C * LP;
     static constexpr size_t SMEM = (size_t)(STAGES * STAGE + PP) * 2 + 2 * (4 * C + 8) * 4 +
-                                   (kSummary ? 0 : NW * C * 4);
+                                   (kSummary ? 0 : NW * C * 8);
 };
 
 __device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_cast<const float2*>(p); }
@@ -215,7 +215,7 @@ la_run_kernel(const LaArgs a) {
     __nv_bfloat16* stages = reinterpret_cast<__nv_bfloat16*>(smem_raw);
     __nv_bfloat16* sP = stages + S::STAGES * S::STAGE;
     GateBuf* gates = reinterpret_cast<GateBuf*>(sP + S::PP);
-    float* sDot = reinterpret_cast<float*>(gates + 2);
+    double* sDot = reinterpret_cast<double*>(gates + 2);
 
     const LaRun& R = a.run[blockIdx.y];
     const int H = a.sp.H;
@@ -493,11 +493,11 @@ la_run_kernel(const LaArgs a) {
                         }
                     }
                     if (w0) {
-                        float dot = 0.f;
+                        double dot = 0.0;
                         if (row < live) {
                             const T* w = w0 + (size_t)row * Hd * DO;
                             const float2 a = pair_of(w), b = pair_of(w + 8);
-                            dot = v[0].x * a.x + v[0].y * a.y + v[1].x * b.x + v[1].y * b.y;
+                            dot = (double)v[0].x * a.x + (double)v[0].y * a.y + (double)v[1].x * b.x + (double)v[1].y * b.y;
                         }
                         dot += __shfl_xor_sync(0xffffffffu, dot, 1);
                         dot += __shfl_xor_sync(0xffffffffu, dot, 2);
@@ -511,12 +511,12 @@ la_run_kernel(const LaArgs a) {
 #pragma unroll
                     for (int e = 0; e < C / 32; ++e) {
                         const int r = lane + 32 * e;
-                        float s = 0.f;
+                        double s = 0.0;
 #pragma unroll
                         for (int w = 0; w < NW; ++w) s += sDot[w * C + r];
                         if (r < live) {
                             R.dot_out[(size_t)(tok + r) * H + h] = s;
-                            sum += (double)s;
+                            sum += s;
                         }
                     }
 #pragma unroll

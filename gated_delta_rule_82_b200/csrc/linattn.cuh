@@ -73,7 +73,7 @@ struct LaRun {
     float p_scale, u_scale, o_scale;   // on the chunk's own products, the state update, the read-out
     const void* dot;             // rows [token][H / dg][output dim] whose products with the output
     int dg;                      // rows are written to dot_out[token][H], or nullptr
-    float* dot_out;
+    double* dot_out;
     double* dot_sum;             // sums of those products over every chunk, by la_chunk_id
 };
 constexpr int kLaMaxRuns = 3;

@@ -76,7 +76,7 @@ la_dg_suffix_kernel(LaSplit sp, double* sq, double* __restrict__ sk,
 // One chunk per CTA, 32 heads at a time (lanes), 8 tokens per warp.  sp.L is the chunk here.
 __global__ void __launch_bounds__(256)
 la_dg_rows_kernel(LaSplit sp, const float* __restrict__ g, int per_token,
-                  const float* __restrict__ rq, const float* __restrict__ rk,
+                  const double* __restrict__ rq, const double* __restrict__ rk,
                   const double* __restrict__ behind, float* __restrict__ dg,
                   double* __restrict__ sums) {
     __shared__ double part[8][32];
@@ -94,7 +94,7 @@ la_dg_rows_kernel(LaSplit sp, const float* __restrict__ g, int per_token,
             const int t = warp * 8 + j;
             if (t < u.len && h < sp.H) {
                 const size_t at = (size_t)(u.tok + t) * sp.H + h;
-                s += (double)rq[at] - (double)rk[at];
+                s += rq[at] - rk[at];
             }
             d[j] = s;
         }
@@ -235,8 +235,8 @@ cudaError_t launch_la_fwd(const LaFwdArgs& f, long long longest, int dk, int dv,
 
 namespace {
 struct BwdWs {
-    float *S, *R, *rq, *rk, *dqf, *dkf;
-    double *decS, *decR, *sq, *sk, *dot;
+    float *S, *R, *dqf, *dkf;
+    double *decS, *decR, *rq, *rk, *sq, *sk, *dot;
     size_t bytes;
 };
 BwdWs bwd_ws(void* ws, bool split, const LaSplit& sp, long long tokens, int G, int dk, int dv) {
@@ -249,8 +249,8 @@ BwdWs bwd_ws(void* ws, bool split, const LaSplit& sp, long long tokens, int G, i
         w.decS = c.take<double>(uh);
         w.decR = c.take<double>(uh);
     }
-    w.rq = c.take<float>(th);
-    w.rk = c.take<float>(th);
+    w.rq = c.take<double>(th);
+    w.rk = c.take<double>(th);
     w.sq = c.take<double>(la_chunk_ids(tokens, sp.n) * H);
     w.sk = c.take<double>(la_chunk_ids(tokens, sp.n) * H);
     w.dot = c.take<double>((size_t)sp.n * H * la_scan_parts(dk * dv));

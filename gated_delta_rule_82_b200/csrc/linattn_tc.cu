@@ -810,10 +810,10 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 32 * e + lane;
-                const float s = (d[t] + d[C + t]) + (d[2 * C + t] + d[3 * C + t]);
+                const double s = ((double)d[t] + d[C + t]) + ((double)d[2 * C + t] + d[3 * C + t]);
                 if (t < live) {
                     R.dot_out[(size_t)(tok + t) * H + h] = s;
-                    sum += (double)s;
+                    sum += s;
                 }
             }
             arrive_warp(&b.dot_empty[slot]);

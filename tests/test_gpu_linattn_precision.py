@@ -147,3 +147,18 @@ def test_sums_of_the_decay_gradient_past_32_bits():
         assert not bool(got[n][:, :-tail].any()), n
     del full, q, k, v, do, got
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_the_decay_gradient(dtype):
+    """Whole numbers again, enough of them for rows of q.dq and k.dk past 2^24 (each of their elements, and
+    the products of 32 channels, below): the rows are sums in fp64 too, and the gradients exact."""
+    T, H, d = 230, 2, 128
+    gen = torch.Generator().manual_seed(3)
+    q, k, v, do = (torch.randint(0, 4, (1, T, H, d), generator=gen).to(dtype).cuda() for _ in range(4))
+    g = torch.zeros(1, T, H, device="cuda")
+    want, _ = ref.backward(q, k, v, g, None, do, None, scale=1.0)
+    parts = [(x.double().cpu() * want[n]).reshape(1, T, H, 4, 32).sum(-1) for x, n in ((q, "dq"), (k, "dk"))]
+    assert all(2 ** 22 < float(p.max()) < 2 ** 24 < float(p.sum(-1).max()) for p in parts)
+    got = ck.linattn_bwd_chunked(q, k, v, g, None, do, scale=1.0)
+    assert torch.equal(got["dlog_decay"].cpu(), want["dlog_decay"].float())
