@@ -23,8 +23,9 @@
 //
 // What bounds it: latency.  A warp holds a state and its operands in 200 registers, so an SM has 8 to
 // 12 warps, 0.27 instructions a cycle and scheduler, the mma.sync pipe 20 to 30 % busy; an fp32 chunk
-// takes six products of terms for one.  16 heads x 4096 tokens: bf16 64 x 64 forward 58 us, backward
-// 192; fp32 128 x 128 forward 237 us, backward 704; fp32 3 x 333 tokens x 6 heads backward 51 us.
+// takes six products of terms for one.  16 heads x 4096 tokens, calls one after the other: bf16 64 x 64
+// forward 65 us, backward 198; fp32 128 x 128 forward 247 us, backward 709; fp32 3 x 333 tokens x 6 heads
+// backward 52 us.
 #include "linattn.cuh"
 
 namespace ckda {
@@ -246,7 +247,8 @@ la_run_kernel(const LaArgs a) {
                 load_rows<T, DC, S::THREADS>(st + NI * (S::XY + S::Z), x, tok, live, H / R.xg,
                                              h / R.xg);
         } else {
-            // (in pieces of up to 16 requests a thread, where a small output leaves few threads)
+            // (x with y and z, or after them in y's registers where y alone takes over 8 requests a
+            // thread.  Few output channels leave few threads: 128 x 16 asks for 64 at once, and spills)
             Fetch<DC, S::THREADS> fy;
             Fetch<DO, S::THREADS> fz;
             fy.request(y, tok, live, H / R.yg, h / R.yg);

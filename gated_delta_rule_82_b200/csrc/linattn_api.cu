@@ -52,12 +52,13 @@ ckda_status read_tokens(int B, int T, const int* cu_host, int n_seqs, int H, Tok
 }
 
 // Units that run side by side.  On tcgen05 (bf16, 128 x 128) a CTA fills an SM; in the backward its
-// longest launch holds two runs (16 heads, 2 x 2048 tokens: 144 us, with 100 units 174, with 148 146;
-// 2 x 1000 tokens: 92, 107, 96).
+// longest launch holds two runs (16 heads, 2 x 2048 tokens, caches flushed: 158 us, with 100 units 182,
+// with 148 156; 2 x 1000 tokens: 94, 113, 100).
 // The warp tiles take a warp for 16 output channels: several narrow heads fit an SM, and a unit
 // leaves its SM waiting for longer than it takes to start another (4096 x 16 heads of 64 x 64:
 // forward 97 us with 148 units, 58 with 296; backward 405 with 74, 224 with 148, 192 with 296; fp32
-// backward of 128 x 128 806 with 74, 680 with 148).
+// backward of 128 x 128 806 with 74, 680 with 148).  All of these are square heads; for others the wider
+// side counts, which leaves SMs idle where the output is the narrow one (128 x 16: a warp a CTA).
 int unit_slots(int dk, int dv, ckda_dtype dtype, bool backward) {
     if (dtype == CKDA_BF16 && dk == 128 && dv == 128) return backward ? 74 : 148;
     return 148 * (128 / (dk > dv ? dk : dv));

@@ -21,10 +21,10 @@
 // that issued all of them would be the slowest part).  They meet on mbarriers only, so a chunk's
 // products overlap the neighbours' element work: per chunk the tensor pipe needs 256 (Sc) + 768 (U)
 // + 530 (O1) + 400 (O2) cycles at NP = 2.
-// What bounds it: the element work of a chunk, about 3700 cycles in the state warps (read U, decay,
-// write the state as an operand, outputs to memory) where HBM alone would allow 2700.  16 heads: 2 x
-// 2048 tokens, forward 42.9 us a call (with one term of the state 38.7), 65536 tokens 400 (359), the
-// summary's launch 16 and 125 of them.
+// What bounds it: the element work of a chunk, about 3800 cycles in the state warps (read U, decay,
+// write the state as an operand, outputs to memory) where HBM alone would allow 2700; tensor pipe 31 %
+// busy, 0.47 instructions a cycle and scheduler.  16 heads: 2 x 2048 tokens, forward 43.0 us a call (with
+// one term of the state 38.7), 65536 tokens 409 (355), the summary's launch 16 and 131 of them.
 // Every wait is bounded; one that runs out is recorded (ckda_last_device_status) and ends the CTA
 // once its copies and products have landed.
 #include <cuda.h>
