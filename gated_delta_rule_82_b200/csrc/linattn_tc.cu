@@ -850,9 +850,6 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
                 if (lane >= o) upto += x;
             }
             const double all = __shfl_sync(0xffffffffu, upto, 31);
-            const double end = __shfl_sync(0xffffffffu, upto, lane | 7);        // of this lane's block
-            double start = __shfl_sync(0xffffffffu, upto, max((lane & ~7) - 1, 0));
-            if (lane < 8) start = 0.0;
             if constexpr (kSummary) decay += all;
             if (i >= kGateRing && !wait(b, &b.gempty[gs], (i / kGateRing - 1) & 1)) break;
             GateSlot& g = gates[gs];
@@ -864,6 +861,9 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
             *reinterpret_cast<float2*>(g.upd + t) =
                 make_float2(t < live ? w.x * u_scale : 0.f, t + 1 < live ? w.y * u_scale : 0.f);
             if constexpr (!kSummary) {
+                const double end = __shfl_sync(0xffffffffu, upto, lane | 7);    // of this lane's block
+                double start = __shfl_sync(0xffffffffu, upto, max((lane & ~7) - 1, 0));
+                if (lane < 8) start = 0.0;
                 const double l0 = G0 - start, l1 = upto - start;
                 const float2 l = make_float2((float)l0, (float)l1);
                 *reinterpret_cast<float2*>(g.l + t) = l;
