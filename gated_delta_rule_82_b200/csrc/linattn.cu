@@ -18,7 +18,7 @@
 // (exact), three for an fp32 one (8 bits each, 24 in all; the products of terms below 2^-24 are
 // left out).  The weighted z of the state update always has three, so states are fp32-grade
 // whatever the input type; P and M as operands have three when `exact` asks for it, else two, which
-// leave 2^-16 of a product, far below a bf16 output's own rounding.  (With one term of M outputs were
+// leave 2^-18 of a value, far below a bf16 output's own rounding.  (With one term of M outputs were
 // 1.24 times as far off as their rounding, with one of P too 1.6 times.)
 //
 // What bounds it: latency.  A warp holds a state and its operands in 200 registers, so an SM has 8 to

@@ -11,7 +11,7 @@
 // operand.  The state lives in the registers of eight warps (a row of 64 channels per thread) and
 // goes to the tensor core as a bf16 operand through TMEM; the weighted Z as well, in three bf16
 // terms (24 bits, 32 columns each), so that states are fp32-grade.  P and the state have NP terms where
-// they are read: two leave 2^-16 of a product, far below an output's own rounding to bf16 (one term of
+// they are read: two leave 2^-18 of a value, far below an output's own rounding to bf16 (one term of
 // the state, the output's own precision, made outputs 1.24 times as far off); three are fp32-grade.
 // The state's lower terms lie in shared memory, half of the second one at NP = 2 in TMEM's last columns.
 //
@@ -199,6 +199,13 @@ __device__ __forceinline__ uint32_t cut2(float2& x) {
     const uint32_t t = __byte_perm(a, b, 0x7632);
     const float2 minus = make_float2(-1.f, -1.f);
     x = fma2(make_float2(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u)), minus, x);
+    return t;
+}
+
+// Both values rounded to bf16, as a pair; x keeps the rest (at most 2^-9 of it).
+__device__ __forceinline__ uint32_t round2(float2& x) {
+    const uint32_t t = pack2(x.x, x.y);
+    x = fma2(make_float2(lo_f(t), hi_f(t)), make_float2(-1.f, -1.f), x);
     return t;
 }
 
@@ -723,9 +730,11 @@ la_tc_kernel(const __grid_constant__ TcArgs args) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)       // (two terms: the second rounds what is left)
+                    for (int q = 0; q < NP; ++q)       // (two terms: both rounded, three: cut)
                         *reinterpret_cast<uint32_t*>(p + q * kBlock + e * 1024 + at) =
-                            NP == 2 && q == 1 ? pack2(w[2 * j + e].x, w[2 * j + e].y) : cut2(w[2 * j + e]);
+                            NP == 3  ? cut2(w[2 * j + e])
+                            : q == 0 ? round2(w[2 * j + e])
+                                     : pack2(w[2 * j + e].x, w[2 * j + e].y);
             }
         };
         auto make_p = [&](int i) {

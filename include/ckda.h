@@ -358,7 +358,7 @@ CKDA_API ckda_status ckda_bwd_chunked(const void* q, const void* k, const void* 
  * Long sequences are cut into units of tokens worked on side by side: summaries of the units, a
  * scan over them, then every unit from its entering state.  States are kept and updated with
  * fp32-grade products for either type; with bf16 inputs scores and states enter the output's
- * products as sums of two bf16 terms (2^-16 of them is left out), so that an output is off by its own
+ * products as sums of two bf16 terms (2^-18 of them is left out), so that an output is off by its own
  * rounding to bf16 alone.  No positive exponent of a decay is formed, so any g <= 0 is safe; a
  * growing g > 0 is accepted and can overflow as the recurrence does.  A non-finite input reaches
  * every later output of its head, and may reach the outputs of earlier tokens of the same chunk of
